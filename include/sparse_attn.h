@@ -25,6 +25,14 @@
  *   sa_csa_compress      CSA: m-token entries merged by a per-channel softmax
  *   sa_csa_window_index  CSA: selected compressed entries plus the raw window,
  *                        as the index list of sa_sparse_mla_decode
+ *   sa_qk_norm_rope      per-head RMS norm of queries and keys with the rotary rotation
+ *   sa_mla_cache_write   latent rows normalised, rotated, quantised (e4m3 with a
+ *                        power-of-two scale per 128 dims) or bf16, into the paged cache
+ *   sa_mla_cache_read    rows of either cache, gathered by position, as bf16
+ *   sa_sparse_mla_q8 / sa_dense_mla_q8
+ *                        sparse / dense MLA attention over the quantised cache
+ *   sa_tree_mla_decode   attention of a tree of drafted tokens over the cached prefix
+ *                        and their own ancestors, either cache
  *
  * Sources, cited by page title and section:
  *   [Notes]  "Sparse Attention 数学学习笔记" (echobase-5bl.pages.dev, 2026.09.14)
@@ -481,6 +489,137 @@ sa_status sa_index_candidates(const void* q, const float* w, const void* k_cache
 
 sa_status sa_topk_from_candidates(const uint64_t* cand, int64_t cand_ld, int32_t* cand_cnt, const int32_t* n_valid,
                                   int rows, int k, int32_t* hist, int32_t* idx_out, sa_stream_t stream);
+
+/*
+ * Per-head RMS norm of queries and keys and the rotary rotation, one pass and
+ * one launch for both ([MLA-S] "为什么 RoPE 要单独处理？": the attention calls of
+ * this library take queries and keys already rotated):
+ *   y = x * rsqrt(mean_d(x^2) + eps) * weight      (norm != 0; weight NULL: ones)
+ *   for every pair (a, b) of the dims [rope_start, rope_start + rope_dims):
+ *     out[a] = y[a] cos - y[b] sin;  out[b] = y[b] cos + y[a] sin
+ * pairs (i, i + rope_dims/2), or (2i, 2i+1) when interleaved != 0, with
+ * cos, sin [n_pos][rope_dims/2] fp32 read at row positions[token].  All in
+ * fp32, rounded once to the storage type.
+ *   q [tokens][H_q][D], k [tokens][H_k][D], dtype SA_BF16 or SA_F32, element
+ *   strides per token and head given, dims contiguous; outputs likewise (out may
+ *   be the input itself; any other overlap is undefined).  H_k = 0 or H_q = 0:
+ *   that side is left out (its pointers may be NULL).  weights [D] fp32 or NULL.
+ *   rope_dims = 0: no rotation (tables and positions may be NULL).
+ * D <= 512.  A position outside [0, n_pos) records code 0x900 in the device
+ * error word and reads row 0.  Any element alignment is accepted; 16-byte
+ * aligned pointers and strides with D a multiple of 8 up to 256 run faster.
+ */
+sa_status sa_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
+                          int64_t q_out_token_stride, int64_t q_out_head_stride, int H_q, const void* k,
+                          int64_t k_token_stride, int64_t k_head_stride, void* k_out, int64_t k_out_token_stride,
+                          int64_t k_out_head_stride, int H_k, sa_dtype dtype, const float* q_weight,
+                          const float* k_weight, int norm, float eps, const float* cos, const float* sin,
+                          int64_t n_pos, const int32_t* positions, int tokens, int D, int rope_start, int rope_dims,
+                          int interleaved, sa_stream_t stream);
+
+/*
+ * Writes tokens into the latent cache ([MLA-S] decode figure: the token's row is
+ * written before it is read).  For token t with slots[t] >= 0 (negative: a
+ * padded token, nothing is written), at the pool row of position slots[t] of
+ * sequence seq_of_row[t]:
+ *   latent   y = c * rsqrt(mean(c^2) + eps) * weight   (norm == 0: y = c)
+ *            stored as bf16 (cache_dtype SA_BF16, c_scale NULL), or as e4m3
+ *            codes (SA_E4M3) with one scale byte per 128 dims in c_scale
+ *            [pool_pages*64][scale_ld]: byte e stands for 2^(e-127), the smallest
+ *            power of two with max|y| <= 448 * 2^(e-127) (1 <= e); code = y / scale
+ *            rounded to nearest, ties to even.  A block that holds a non-finite
+ *            value gets byte 255 and reads as NaN.
+ *   RoPE key kr rotated as in sa_qk_norm_rope at positions[t] (NULL: slots[t]),
+ *            cos, sin [n_pos][32] fp32, stored as bf16
+ *   c [tokens][512], kr [tokens][64], in_dtype SA_BF16 or SA_F32, row strides
+ *   c_in_ld, kr_in_ld; weight [512] fp32 or NULL (ones).
+ * Two tokens of one call must not name the same row (precondition).  A slot past
+ * the page table, or on a page outside the pool, is not written and records code
+ * 0x700; a position outside the tables records 0x900 and reads row 0.  Alignment:
+ * c, weight, c_cache, kr_cache and the c and cache row strides 16 bytes, c_scale
+ * and scale_ld 4 bytes.  d_c = 512, d_R = 64.
+ */
+sa_status sa_mla_cache_write(const void* c, int64_t c_in_ld, const void* kr, int64_t kr_in_ld, sa_dtype in_dtype,
+                             const float* weight, int norm, float eps, const float* cos, const float* sin,
+                             int64_t n_pos, const int32_t* positions, int interleaved, void* c_cache,
+                             sa_dtype cache_dtype, int64_t c_ld, uint8_t* c_scale, int64_t scale_ld, void* kr_cache,
+                             int64_t kr_ld, int64_t pool_pages, const int32_t* page_table, int pages_per_seq,
+                             const int32_t* seq_of_row, const int32_t* slots, int tokens, int d_c, int d_R,
+                             sa_stream_t stream);
+
+/*
+ * Rows of the latent cache by position: c_out [rows][k][512] and kr_out
+ * [rows][k][64] (may be NULL), bf16, hold the cached rows of positions idx
+ * [rows][k] of sequence seq_of_row[r]; -1 gives zeros.  A quantised value is
+ * code * 2^(e-127), which bf16 holds exactly, so this reads back what the
+ * attention calls over the cache see.  A position past the page table, or on a
+ * page outside the pool, records code 0x700 and reads row 0 of the pool.  Layout
+ * and alignment of the cache as in sa_mla_cache_write; outputs 16 bytes.
+ */
+sa_status sa_mla_cache_read(const void* c_cache, sa_dtype cache_dtype, int64_t c_ld, const uint8_t* c_scale,
+                            int64_t scale_ld, const void* kr_cache, int64_t kr_ld, int64_t pool_pages,
+                            const int32_t* page_table, int pages_per_seq, const int32_t* seq_of_row,
+                            const int32_t* idx, int rows, int k, int d_c, int d_R, void* c_out, void* kr_out,
+                            sa_stream_t stream);
+
+/*
+ * Sparse MLA attention (sa_sparse_mla_decode / _prefill: same query, selection,
+ * output and lse) over the quantised cache of sa_mla_cache_write, for any number
+ * of rows: c_cache rows of 512 e4m3 codes at stride c_ld bytes, c_scale rows of
+ * four scale bytes at stride scale_ld, kr_cache rows of 64 bf16.  The latent row
+ * enters both products with the exact value code * 2^(e-127) (codes 0x7F and
+ * 0xFF, which the write call never stores, are not valid contents).  out is fp32
+ * (SA_F32) or bf16 (SA_BF16: rounded once).  sa_dense_mla_q8 attends to positions
+ * 0 .. n_visible[r]-1 instead of a selection.  The workspace (256-byte aligned,
+ * scratch) may be NULL when its size is 0; concurrent calls need separate ones.
+ */
+size_t sa_sparse_mla_q8_workspace_size(int rows, int H, int k);
+
+sa_status sa_sparse_mla_q8(const void* q_lat, const void* q_rope, const void* c_cache, int64_t c_ld,
+                           const uint8_t* c_scale, int64_t scale_ld, const void* kr_cache, int64_t kr_ld,
+                           int64_t pool_pages, const int32_t* page_table, int pages_per_seq,
+                           const int32_t* seq_of_row, const int32_t* idx, int rows, int H, int k, int d_c, int d_R,
+                           float scale, void* out, sa_dtype out_dtype, float* lse, void* workspace,
+                           size_t workspace_bytes, sa_stream_t stream);
+
+size_t sa_dense_mla_q8_workspace_size(int rows, int H, int L_max);
+
+sa_status sa_dense_mla_q8(const void* q_lat, const void* q_rope, const void* c_cache, int64_t c_ld,
+                          const uint8_t* c_scale, int64_t scale_ld, const void* kr_cache, int64_t kr_ld,
+                          int64_t pool_pages, const int32_t* page_table, int pages_per_seq, const int32_t* seq_of_row,
+                          const int32_t* n_visible, int rows, int H, int L_max, int d_c, int d_R, float scale,
+                          void* out, sa_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                          sa_stream_t stream);
+
+/*
+ * MLA attention of drafted tokens (verification of a drafted tree): sequence b
+ * has n_past[b] cached positions and n_draft[b] <= T drafted tokens (NULL: T),
+ * whose rows sit in the cache at positions n_past[b] + j (sa_mla_cache_write with
+ * slots = n_past + j and positions = n_past + depth).  Token i attends to
+ * positions 0 .. n_past[b]-1 and to the drafted tokens j < n_draft[b] with
+ * tree_mask[b][i][j] != 0 (uint8 [B][T][T]: its ancestors and itself; NULL: j <= i,
+ * a chain).  Scores, softmax and output as sa_sparse_mla_decode.
+ *   q_lat [B][T][H][512], q_rope [B][T][H][64] bf16; out [B][T][H][512] fp32 or
+ *   bf16; lse [B][T][H] fp32 or NULL.  Rows i >= n_draft[b] are not written.
+ *   seq_of_row [B]: the sequence of tree b (NULL: b).  A token with nothing to
+ *   attend to gets zeros and lse -inf.  Masked rows never reach a result, NaN or
+ *   infinite contents included.
+ *   L_max >= n_past[b] + n_draft[b] for every b sets the key split and the
+ *   workspace; a longer sequence still gives right results.
+ * cache_dtype SA_BF16 (c_scale NULL, c_ld in elements) or SA_E4M3.
+ * 1 <= T <= SA_TREE_MAX_TOKENS, H <= 128.  Workspace as sa_sparse_mla_q8.
+ */
+#define SA_TREE_MAX_TOKENS 1024
+
+size_t sa_tree_mla_workspace_size(int B, int T, int H, int L_max);
+
+sa_status sa_tree_mla_decode(const void* q_lat, const void* q_rope, const void* c_cache, sa_dtype cache_dtype,
+                             int64_t c_ld, const uint8_t* c_scale, int64_t scale_ld, const void* kr_cache,
+                             int64_t kr_ld, int64_t pool_pages, const int32_t* page_table, int pages_per_seq,
+                             const int32_t* seq_of_row, const int32_t* n_past, const int32_t* n_draft,
+                             const uint8_t* tree_mask, int B, int T, int H, int L_max, int d_c, int d_R, float scale,
+                             void* out, sa_dtype out_dtype, float* lse, void* workspace, size_t workspace_bytes,
+                             sa_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -32,7 +32,9 @@ EXPORTS = (
     "sa_nsa_compress", "sa_nsa_decode", "sa_csa_compress", "sa_csa_window_index",
     "sa_index_scores_hist", "sa_topk_select_hist", "sa_set_wait_limit_ns",
     "sa_index_candidates", "sa_topk_from_candidates", "sa_sparse_mla_decode_bf16", "sa_sparse_mla_prefill_bf16",
-    "sa_mla_up_project_bf16",
+    "sa_mla_up_project_bf16", "sa_qk_norm_rope", "sa_mla_cache_write", "sa_mla_cache_read",
+    "sa_sparse_mla_q8_workspace_size", "sa_sparse_mla_q8", "sa_dense_mla_q8_workspace_size", "sa_dense_mla_q8",
+    "sa_tree_mla_workspace_size", "sa_tree_mla_decode",
 )
 
 # Size of the library's static device array behind sparse_mla_decode_static
@@ -87,9 +89,21 @@ def lib():
         L.sa_nsa_decode.argtypes = [P, P, P, I64, I64, I64, P, P, I64, P, I, I, I, I, I, I, I, I, F, P, P, P]
         L.sa_csa_compress.argtypes = [P, P, P, P, I64, I64, P, P, I, I, I, I, I, I, P, I, I64, I64, P]
         L.sa_csa_window_index.argtypes = [P, I, I, P, I, I, P, P]
+        L.sa_qk_norm_rope.argtypes = [P, I64, I64, P, I64, I64, I, P, I64, I64, P, I64, I64, I, I, P, P, I, F, P, P,
+                                      I64, P, I, I, I, I, I, P]
+        L.sa_mla_cache_write.argtypes = [P, I64, P, I64, I, P, I, F, P, P, I64, P, I, P, I, I64, P, I64, P, I64, I64,
+                                         P, I, P, P, I, I, I, P]
+        L.sa_mla_cache_read.argtypes = [P, I, I64, P, I64, P, I64, I64, P, I, P, P, I, I, I, I, P, P, P]
+        L.sa_sparse_mla_q8.argtypes = [P, P, P, I64, P, I64, P, I64, I64, P, I, P, P, I, I, I, I, I, F, P, I, P, P,
+                                       SZ, P]
+        L.sa_dense_mla_q8.argtypes = L.sa_sparse_mla_q8.argtypes
+        L.sa_tree_mla_decode.argtypes = [P, P, P, I, I64, P, I64, P, I64, I64, P, I, P, P, P, P, I, I, I, I, I, I, F,
+                                         P, I, P, P, SZ, P]
+        for name, args in (("sparse_mla_q8", [I, I, I]), ("dense_mla_q8", [I, I, I]), ("tree_mla", [I, I, I, I])):
+            getattr(L, f"sa_{name}_workspace_size").argtypes = args
+            getattr(L, f"sa_{name}_workspace_size").restype = SZ
         for name in EXPORTS:
-            if name not in ("sa_status_string", "sa_version", "sa_sparse_mla_workspace_size",
-                            "sa_sparse_mla_prefill_workspace_size", "sa_dense_mla_workspace_size"):
+            if name not in ("sa_status_string", "sa_version") and not name.endswith("_workspace_size"):
                 getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -231,9 +245,13 @@ def _mla_args(q_lat, q_rope, c_cache, kr_cache, idx, out, lse):
 
 
 def sparse_mla_decode(q_lat, q_rope, c_cache, kr_cache, idx, scale: float, pages_per_seq: int, page_table=None,
-                      seq_of_row=None, out=None, lse=None, workspace=None):
+                      seq_of_row=None, out=None, lse=None, workspace=None, c_scale=None):
     """Sparse MLA (latent aggregate) [rows, H, d_c], fp32 (or bf16 when `out`
-    is a bf16 tensor); optional lse [rows, H]."""
+    is a bf16 tensor); optional lse [rows, H].  With `c_scale` the cache is the
+    quantised one of mla_cache_write (workspace: sparse_mla_q8_workspace_size)."""
+    if c_scale is not None:
+        return _sparse_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, idx, scale, pages_per_seq, page_table,
+                              seq_of_row, out, lse, workspace)
     rows, H, d_c, d_R, k, out, lse, pool_pages = _mla_args(q_lat, q_rope, c_cache, kr_cache, idx, out, lse)
     need = sparse_mla_workspace_size(rows, H, k, d_c)
     if workspace is None and need > 0:
@@ -253,7 +271,11 @@ def sparse_mla_prefill_workspace_size(rows: int, H: int, k: int, d_c: int = 512)
 
 
 def sparse_mla_prefill(q_lat, q_rope, c_cache, kr_cache, idx, scale: float, pages_per_seq: int, page_table=None,
-                       seq_of_row=None, out=None, lse=None, workspace=None):
+                       seq_of_row=None, out=None, lse=None, workspace=None, c_scale=None):
+    """sparse_mla_decode for many rows (one key split per row)."""
+    if c_scale is not None:
+        return _sparse_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, idx, scale, pages_per_seq, page_table,
+                              seq_of_row, out, lse, workspace)
     rows, H, d_c, d_R, k, out, lse, pool_pages = _mla_args(q_lat, q_rope, c_cache, kr_cache, idx, out, lse)
     if workspace is None and rows > 0:
         workspace = torch.empty(sparse_mla_prefill_workspace_size(rows, H, k, d_c), dtype=torch.uint8,
@@ -273,9 +295,14 @@ def dense_mla_workspace_size(rows: int, H: int, L_max: int, d_c: int = 512) -> i
 
 
 def dense_mla_decode(q_lat, q_rope, c_cache, kr_cache, n_visible, L_max: int, scale: float, pages_per_seq: int,
-                     page_table=None, seq_of_row=None, out=None, lse=None, workspace=None):
+                     page_table=None, seq_of_row=None, out=None, lse=None, workspace=None, c_scale=None):
     """Dense MLA over every visible position (the short-sequence mode): row r
-    attends to positions 0 .. n_visible[r]-1.  [rows, H, d_c] fp32."""
+    attends to positions 0 .. n_visible[r]-1.  [rows, H, d_c] fp32.  With
+    `c_scale` the cache is the quantised one of mla_cache_write (`out` may then
+    be bf16; workspace: dense_mla_q8_workspace_size)."""
+    if c_scale is not None:
+        return _dense_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, n_visible, L_max, scale, pages_per_seq,
+                             page_table, seq_of_row, out, lse, workspace)
     rows, H, d_c = q_lat.shape
     d_R = q_rope.shape[2]
     if out is None:
@@ -424,3 +451,222 @@ def csa_window_index(topk_idx, raw_len, window: int, win_base: int, idx_out=None
     st = lib().sa_csa_window_index(_p(topk_idx), rows, k, _p(raw_len), window, win_base, _p(idx_out), _stream())
     _check("sa_csa_window_index", st)
     return idx_out
+
+
+def _need(t, name: str, dtypes, shape=None, contiguous=True):
+    """Check one tensor argument: on the current device, of an allowed dtype,
+    of the given shape (None: any extent) and, unless strides are passed on,
+    contiguous."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape))):
+        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
+                         f"not {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t
+
+
+_SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+_IO_TYPES = (torch.bfloat16, torch.float32)
+
+
+def _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows):
+    """Check a latent cache; return (dtype code, c_ld, scale_ld, kr_ld, pool_pages)."""
+    n = c_cache.shape[0]
+    quantised = c_cache.dtype == torch.float8_e4m3fn
+    if quantised != (c_scale is not None):
+        raise ValueError("an e4m3 cache needs c_scale, a bf16 cache has none")
+    if n == 0 or n % 64:
+        raise ValueError(f"the cache holds whole pages of 64 rows, not {n} rows")
+    _need(c_cache, "c_cache", (torch.float8_e4m3fn, torch.bfloat16), (n, 512), contiguous=False)
+    _need(kr_cache, "kr_cache", (torch.bfloat16,), (n, 64), contiguous=False)
+    pools = [c_cache, kr_cache]
+    if quantised:
+        pools.append(_need(c_scale, "c_scale", _SCALE_TYPES, (n, 4), contiguous=False))
+    if any(t.stride(1) != 1 for t in pools):
+        raise ValueError("the dims of a cache row must be contiguous")
+    if page_table is not None:
+        _need(page_table, "page_table", (torch.int32,), (None, pages_per_seq))
+    if seq_of_row is not None:
+        _need(seq_of_row, "seq_of_row", (torch.int32,), (rows,))
+    elif page_table is not None and page_table.shape[0] < rows:
+        raise ValueError(f"page_table has {page_table.shape[0]} sequences for {rows} rows")
+    return (SA_E4M3 if quantised else SA_BF16, c_cache.stride(0), c_scale.stride(0) if quantised else 0,
+            kr_cache.stride(0), n // 64)
+
+
+def _need_tables(cos, sin, half):
+    _need(cos, "cos", (torch.float32,), (None, half))
+    _need(sin, "sin", (torch.float32,), tuple(cos.shape))
+
+
+def _code(t) -> int:
+    return SA_F32 if t.dtype == torch.float32 else SA_BF16
+
+
+def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                 rope_start: int = 0, interleaved: bool = False, q_out=None, k_out=None):
+    """Per-head RMS norm (skipped if not `norm`) and rotary rotation of queries
+    q [tokens, H_q, D] and keys k [tokens, H_k, D] (or None), bf16 or fp32, in
+    one launch.  Dims rope_start .. rope_start + 2*cos.shape[1] - 1 are rotated
+    by row positions[t] of cos and sin [n_pos, rope_dims/2] fp32, in split
+    halves or interleaved pairs; cos = sin = None: no rotation.  Token and
+    head strides are free; q_out and k_out may be q and k.  Returns (q_out, k_out)."""
+    tokens, Hq, D = q.shape
+    rope = 0 if cos is None else 2 * cos.shape[1]
+    ins, outs = [_need(q, "q", _IO_TYPES, contiguous=False)], [q_out]
+    if k is not None:
+        ins.append(_need(k, "k", (q.dtype,), (tokens, None, D), contiguous=False))
+        outs.append(k_out)
+    for i, (x, o) in enumerate(zip(ins, outs)):
+        outs[i] = torch.empty(x.shape, dtype=x.dtype, device=x.device) if o is None else \
+            _need(o, "output", (x.dtype,), tuple(x.shape), contiguous=False)
+    if any(t.stride(2) != 1 and D > 1 for t in ins + outs):
+        raise ValueError("the dims of a head must be contiguous")
+    if any(t.stride(i) == 0 and t.shape[i] > 1 for t in outs for i in (0, 1)):
+        raise ValueError("an output must not be a broadcast view")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, (torch.float32,), (D,))
+    if rope:
+        _need_tables(cos, sin, rope // 2)
+        _need(positions, "positions", (torch.int32,), (tokens,))
+    side = lambda x, o: (_p(x), x.stride(0), x.stride(1), _p(o), o.stride(0), o.stride(1), x.shape[1])  # noqa: E731
+    keys = (None, 0, 0, None, 0, 0, 0) if k is None else side(ins[1], outs[1])
+    st = lib().sa_qk_norm_rope(*side(ins[0], outs[0]), *keys, _code(q), _p(q_weight), _p(k_weight), int(bool(norm)),
+                               float(eps), _p(cos), _p(sin), cos.shape[0] if rope else 0, _p(positions), tokens, D,
+                               rope_start, rope, int(bool(interleaved)), _stream())
+    _check("sa_qk_norm_rope", st)
+    return outs[0], (None if k is None else outs[1])
+
+
+def mla_cache_write(c, kr, c_cache, kr_cache, slots, pages_per_seq: int, cos, sin, positions=None, weight=None,
+                    eps: float = 1e-6, norm: bool = True, interleaved: bool = False, c_scale=None, page_table=None,
+                    seq_of_row=None):
+    """Write tokens into the latent cache: c [tokens, 512] RMS-normalised
+    (skipped if not `norm`) and stored as bf16, or as e4m3 codes with a scale
+    byte per 128 dims when c_scale ([rows, 4] uint8 or float8_e8m0fnu) is
+    given; kr [tokens, 64] rotated by row positions[t] (None: slots[t]) of
+    cos and sin [n_pos, 32].  slots [tokens] int32: position of the token in
+    sequence seq_of_row[t] (None: t), -1: skip the token."""
+    tokens = c.shape[0]
+    _need(c, "c", _IO_TYPES, (tokens, 512), contiguous=False)
+    _need(kr, "kr", (c.dtype,), (tokens, 64), contiguous=False)
+    if c.stride(1) != 1 or kr.stride(1) != 1:
+        raise ValueError("the dims of a token must be contiguous")
+    _need(slots, "slots", (torch.int32,), (tokens,))
+    if positions is not None:
+        _need(positions, "positions", (torch.int32,), (tokens,))
+    if weight is not None:
+        _need(weight, "weight", (torch.float32,), (512,))
+    _need_tables(cos, sin, 32)
+    dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, tokens)
+    st = lib().sa_mla_cache_write(_p(c), max(c.stride(0), 512), _p(kr), max(kr.stride(0), 64), _code(c), _p(weight),
+                                  int(bool(norm)), float(eps), _p(cos), _p(sin), cos.shape[0], _p(positions),
+                                  int(bool(interleaved)), _p(c_cache), dt, c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld,
+                                  pool, _p(page_table), pages_per_seq, _p(seq_of_row), _p(slots), tokens, 512, 64,
+                                  _stream())
+    _check("sa_mla_cache_write", st)
+
+
+def mla_cache_read(c_cache, kr_cache, idx, pages_per_seq: int, c_scale=None, page_table=None, seq_of_row=None,
+                   c_out=None, kr_out=None):
+    """Rows of the latent cache at positions idx [rows, k] int32 (-1: zeros) of
+    sequence seq_of_row[r], as bf16: (c [rows, k, 512], kr [rows, k, 64])."""
+    rows, k = idx.shape
+    _need(idx, "idx", (torch.int32,))
+    dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
+    if c_out is None:
+        c_out = torch.empty(rows, k, 512, dtype=torch.bfloat16, device=idx.device)
+    if kr_out is None:
+        kr_out = torch.empty(rows, k, 64, dtype=torch.bfloat16, device=idx.device)
+    _need(c_out, "c_out", (torch.bfloat16,), (rows, k, 512))
+    _need(kr_out, "kr_out", (torch.bfloat16,), (rows, k, 64))
+    st = lib().sa_mla_cache_read(_p(c_cache), dt, c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld, pool, _p(page_table),
+                                 pages_per_seq, _p(seq_of_row), _p(idx), rows, k, 512, 64, _p(c_out), _p(kr_out),
+                                 _stream())
+    _check("sa_mla_cache_read", st)
+    return c_out, kr_out
+
+
+def sparse_mla_q8_workspace_size(rows: int, H: int, k: int) -> int:
+    return int(lib().sa_sparse_mla_q8_workspace_size(rows, H, k))
+
+
+def dense_mla_q8_workspace_size(rows: int, H: int, L_max: int) -> int:
+    return int(lib().sa_dense_mla_q8_workspace_size(rows, H, L_max))
+
+
+def tree_mla_workspace_size(B: int, T: int, H: int, L_max: int) -> int:
+    return int(lib().sa_tree_mla_workspace_size(B, T, H, L_max))
+
+
+def _latent_io(q_lat, q_rope, out, lse, workspace, need: int):
+    """Check queries [..., H, 512] / [..., H, 64]; make the output and the workspace when not given."""
+    lead = tuple(q_lat.shape[:-1])
+    _need(q_lat, "q_lat", (torch.bfloat16,), lead + (512,))
+    _need(q_rope, "q_rope", (torch.bfloat16,), lead + (64,))
+    if out is None:
+        out = torch.empty(lead + (512,), dtype=torch.float32, device=q_lat.device)
+    _need(out, "out", _IO_TYPES, lead + (512,))
+    if lse is not None:
+        _need(lse, "lse", (torch.float32,), lead)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
+    if workspace is not None:
+        _need(workspace, "workspace", (workspace.dtype,))
+    return out, workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _sparse_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, idx, scale, pages_per_seq, page_table, seq_of_row, out,
+                   lse, workspace):
+    rows, H, _ = q_lat.shape
+    _need(idx, "idx", (torch.int32,), (rows, None))
+    k = idx.shape[1]
+    out, workspace, wbytes = _latent_io(q_lat, q_rope, out, lse, workspace, sparse_mla_q8_workspace_size(rows, H, k))
+    _, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
+    st = lib().sa_sparse_mla_q8(_p(q_lat), _p(q_rope), _p(c_cache), c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld, pool,
+                                _p(page_table), pages_per_seq, _p(seq_of_row), _p(idx), rows, H, k, 512, 64,
+                                float(scale), _p(out), _code(out), _p(lse), _p(workspace), wbytes, _stream())
+    _check("sa_sparse_mla_q8", st)
+    return out
+
+
+def _dense_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, n_visible, L_max, scale, pages_per_seq, page_table,
+                  seq_of_row, out, lse, workspace):
+    rows, H, _ = q_lat.shape
+    _need(n_visible, "n_visible", (torch.int32,), (rows,))
+    out, workspace, wbytes = _latent_io(q_lat, q_rope, out, lse, workspace, dense_mla_q8_workspace_size(rows, H, L_max))
+    _, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
+    st = lib().sa_dense_mla_q8(_p(q_lat), _p(q_rope), _p(c_cache), c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld, pool,
+                               _p(page_table), pages_per_seq, _p(seq_of_row), _p(n_visible), rows, H, L_max, 512, 64,
+                               float(scale), _p(out), _code(out), _p(lse), _p(workspace), wbytes, _stream())
+    _check("sa_dense_mla_q8", st)
+    return out
+
+
+def tree_mla_decode(q_lat, q_rope, c_cache, kr_cache, n_past, tree_mask, L_max: int, scale: float, pages_per_seq: int,
+                    n_draft=None, c_scale=None, page_table=None, seq_of_row=None, out=None, lse=None, workspace=None):
+    """MLA attention of drafted tokens: q_lat [B, T, H, 512], q_rope [B, T, H, 64]
+    bf16.  Token i of tree b attends to cached positions 0 .. n_past[b]-1 and to
+    the drafted tokens j < n_draft[b] (None: T), cached at n_past[b] + j, with
+    tree_mask[b, i, j] nonzero (uint8 or bool [B, T, T]; None: j <= i).  The
+    cache is bf16, or e4m3 with `c_scale`.  [B, T, H, 512] fp32 (or bf16 when
+    `out` is a bf16 tensor); rows i >= n_draft[b] are left as they were."""
+    B, T, H, _ = q_lat.shape
+    _need(n_past, "n_past", (torch.int32,), (B,))
+    if n_draft is not None:
+        _need(n_draft, "n_draft", (torch.int32,), (B,))
+    if tree_mask is not None:
+        _need(tree_mask, "tree_mask", (torch.uint8, torch.bool), (B, T, T))
+    out, workspace, wbytes = _latent_io(q_lat, q_rope, out, lse, workspace, tree_mla_workspace_size(B, T, H, L_max))
+    dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, B)
+    st = lib().sa_tree_mla_decode(_p(q_lat), _p(q_rope), _p(c_cache), dt, c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld,
+                                  pool, _p(page_table), pages_per_seq, _p(seq_of_row), _p(n_past), _p(n_draft),
+                                  _p(tree_mask), B, T, H, L_max, 512, 64, float(scale), _p(out), _code(out), _p(lse),
+                                  _p(workspace), wbytes, _stream())
+    _check("sa_tree_mla_decode", st)
+    return out

@@ -28,7 +28,8 @@ enum : int {
     kErrGemmWait = 0x500,    // per-head projection GEMM waits
     kErrNsaWait = 0x600,     // NSA decode waits (low byte = ring slot)
     kErrMlaIndex = 0x700,    // sparse MLA: a position past the page table or a page outside the pool
-    kErrBlockWait = 0x800    // block-sparse decode waits (low byte = site)
+    kErrBlockWait = 0x800,   // block-sparse decode waits (low byte = site)
+    kErrRopePos = 0x900      // rotary position outside the cos/sin tables
 };
 
 constexpr unsigned long long kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
@@ -470,6 +471,33 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 // Named barrier over `nthreads` threads (multiple of 32), id 1..15.
 __device__ __forceinline__ void named_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// ---------------------------------------------------------------- quantised latent rows
+// A scale byte e stands for 2^(e-127); 255 marks a block that held a
+// non-finite value and reads as NaN.  The scale as two packed bf16: the byte
+// is the exponent field (e = 0 is never written; it reads as scale 0).
+__device__ __forceinline__ uint32_t q8_scale_bf16x2(uint32_t e) {
+    const uint32_t b = e == 255u ? 0x7FC0u : e << 7;
+    return b | (b << 16);
+}
+
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Four e4m3 codes -> four bf16, times the scale.  A code's exponent and
+// mantissa bits shifted into the bf16 fields are its value times 2^-120
+// (subnormal codes become subnormal bf16), so a product with 2^120 restores
+// it; both products are by powers of two and exact.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, uint32_t scale2) {
+    constexpr uint32_t k2p120 = 0x7B807B80u;
+    const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
+    const uint32_t l = ((lo >> 4) & 0x07F007F0u) | (lo & 0x80008000u);
+    const uint32_t h = ((hi >> 4) & 0x07F007F0u) | (hi & 0x80008000u);
+    return make_uint2(hmul2_bf16(hmul2_bf16(l, k2p120), scale2), hmul2_bf16(hmul2_bf16(h, k2p120), scale2));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

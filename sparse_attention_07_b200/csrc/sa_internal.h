@@ -133,4 +133,114 @@ sa_status csa_compress_launch(const void* Ca, const void* Cb, const void* Za, co
 sa_status csa_window_index_launch(const int32_t* topk_idx, int rows, int k, const int32_t* raw_len, int window,
                                   int win_base, int32_t* idx_out, cudaStream_t st);
 
+// Per-head RMS norm and rotation (norm_rope.cu).  Strides in elements; Hk = 0:
+// no keys; rot = 0: no rotation.
+struct NormRopeArgs {
+    const void* q;
+    int64_t q_ts, q_hs;
+    void* q_out;
+    int64_t qo_ts, qo_hs;
+    int Hq;
+    const void* k;
+    int64_t k_ts, k_hs;
+    void* k_out;
+    int64_t ko_ts, ko_hs;
+    int Hk;
+    const float* q_weight;  // [D] or null
+    const float* k_weight;
+    int norm;
+    float eps;
+    const float* cos;  // [n_pos][rot / 2]
+    const float* sin;
+    int64_t n_pos;
+    const int32_t* positions;
+    int tokens, D, start, rot, interleaved;
+    int* err;
+};
+sa_status norm_rope_launch(const NormRopeArgs& a, sa_dtype dt, cudaStream_t st);
+
+// The latent cache written and read back (mla_cache.cu).
+struct CacheWriteArgs {
+    const void* c;
+    int64_t c_in_ld;
+    const void* kr;
+    int64_t kr_in_ld;
+    const float* weight;
+    int norm;
+    float eps;
+    const float* cos;  // [n_pos][32]
+    const float* sin;
+    int64_t n_pos;
+    const int32_t* positions;  // null: the slots
+    int interleaved;
+    void* c_cache;
+    int64_t c_ld;
+    uint8_t* c_scale;  // null: the cache rows are bf16
+    int64_t s_ld;
+    void* kr_cache;
+    int64_t kr_ld;
+    int64_t pool_pages;
+    const int32_t* page_table;
+    int pages_per_seq;
+    const int32_t* seq_of_row;
+    const int32_t* slots;
+    int tokens;
+    int* err;
+};
+sa_status mla_cache_write_launch(const CacheWriteArgs& a, sa_dtype dt, cudaStream_t st);
+
+struct CacheReadArgs {
+    const void* c_cache;
+    int64_t c_ld;
+    const uint8_t* c_scale;  // null: the cache rows are bf16
+    int64_t s_ld;
+    const void* kr_cache;
+    int64_t kr_ld;
+    int64_t pool_pages;
+    const int32_t* page_table;
+    int pages_per_seq;
+    const int32_t* seq_of_row;
+    const int32_t* idx;
+    int rows, k;
+    void* c_out;
+    void* kr_out;  // may be null
+    int* err;
+};
+sa_status mla_cache_read_launch(const CacheReadArgs& a, cudaStream_t st);
+
+// MLA attention over the quantised cache, and of drafted trees over either
+// cache (mla_latent.cu).  Query row r = (sequence b, token i), r = b * T + i.
+//   selection:  idx [rows][k], T = 1
+//   otherwise:  n_past[b] cached positions, then (tree) n_draft[b] drafted
+//               ones, of which token i sees j where tree_mask[b][i][j] is
+//               nonzero (null: j <= i)
+struct LatentArgs {
+    const void* q_lat;
+    const void* q_rope;
+    const void* c_cache;
+    int64_t c_ld;
+    const uint8_t* c_scale;  // null: the cache rows are bf16
+    int64_t s_ld;
+    const void* kr_cache;
+    int64_t kr_ld;
+    const int32_t* page_table;
+    int pages_per_seq;
+    int64_t pool_pages;
+    const int32_t* seq_of_row;  // [B]
+    const int32_t* idx;
+    int k;                      // selection: slots per row; else the longest row
+    const int32_t* n_past;
+    const int32_t* n_draft;     // null: T
+    const uint8_t* tree_mask;
+    int tree;                   // drafted tokens are keys too
+    int B, T, H;
+    float scale;
+    float* out;
+    void* out_bf16;
+    float* lse;
+    int* err;
+};
+size_t mla_latent_workspace_bytes(int B, int T, int H, int k, bool shared_keys);
+sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cudaStream_t st);
+
 }  // namespace sa
