@@ -181,7 +181,7 @@ static sa_status latent_attn(const void* q_lat, const void* q_rope, const void* 
         !aligned(n_past, 4) || !aligned(n_draft, 4))
         return SA_EINVAL;
     if (static_cast<int64_t>(B) * T > (int64_t(1) << 24)) return SA_EUNSUPPORTED;
-    const size_t need = mla_latent_workspace_bytes(B, T, H, k, idx == nullptr);
+    const size_t need = mla_latent_workspace_bytes(B, T, H, k);
     if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return SA_EINVAL;
     LatentArgs a = {};
     a.q_lat = q_lat;
@@ -215,7 +215,7 @@ static sa_status latent_attn(const void* q_lat, const void* q_rope, const void* 
 
 size_t sa_sparse_mla_q8_workspace_size(int rows, int H, int k) {
     if (rows < 1 || H < 1 || k < 1) return 0;
-    return mla_latent_workspace_bytes(rows, 1, H, k, false);
+    return mla_latent_workspace_bytes(rows, 1, H, k);
 }
 
 sa_status sa_sparse_mla_q8(const void* q_lat, const void* q_rope, const void* c_cache, int64_t c_ld,
@@ -245,7 +245,7 @@ sa_status sa_dense_mla_q8(const void* q_lat, const void* q_rope, const void* c_c
 
 size_t sa_tree_mla_workspace_size(int B, int T, int H, int L_max) {
     if (B < 1 || T < 1 || H < 1 || L_max < 1) return 0;
-    return mla_latent_workspace_bytes(B, T, H, L_max, true);
+    return mla_latent_workspace_bytes(B, T, H, L_max);
 }
 
 sa_status sa_tree_mla_decode(const void* q_lat, const void* q_rope, const void* c_cache, sa_dtype cache_dtype,

@@ -29,7 +29,8 @@ enum : int {
     kErrNsaWait = 0x600,     // NSA decode waits (low byte = ring slot)
     kErrMlaIndex = 0x700,    // sparse MLA: a position past the page table or a page outside the pool
     kErrBlockWait = 0x800,   // block-sparse decode waits (low byte = site)
-    kErrRopePos = 0x900      // rotary position outside the cos/sin tables
+    kErrRopePos = 0x900,     // rotary position outside the cos/sin tables
+    kErrLatWait = 0xA00      // latent-cache attention waits (low byte = site)
 };
 
 constexpr unsigned long long kWaitLimitNs = 1000ull * 1000ull * 1000ull;  // 1 s
@@ -257,6 +258,11 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// As fence_proxy_async_smem, for writes to the shared memory of any CTA of the cluster.
+__device__ __forceinline__ void fence_proxy_async_cluster() {
+    asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+}
+
 // Order this thread's generic-proxy shared-memory writes before later
 // async-proxy (tensor core / TMA) reads of the same memory.
 __device__ __forceinline__ void fence_proxy_async_smem() {
@@ -339,6 +345,39 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t adesc, uint6
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// ---- CTA pairs (cta_group::2).  An M = 128 product puts 64 rows of D in each
+// CTA: lane l < 64 holds row l, columns 0 .. N/2-1, lane 64 + l the same row,
+// columns N/2 .. N-1.  Each CTA supplies its 64 rows of A and half the N rows
+// of B from its own shared memory, at the same offsets in both; one thread of
+// the even CTA issues.
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
+                 "r"(ncols)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive once on `bar` of both CTAs when every pair op this thread issued so far is done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
         : "memory");
 }
 

@@ -240,7 +240,7 @@ struct LatentArgs {
     float* lse;
     int* err;
 };
-size_t mla_latent_workspace_bytes(int B, int T, int H, int k, bool shared_keys);
+size_t mla_latent_workspace_bytes(int B, int T, int H, int k);
 sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cudaStream_t st);
 
 }  // namespace sa
