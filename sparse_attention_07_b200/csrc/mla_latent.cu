@@ -12,22 +12,31 @@
 //    fp32 = 256 tensor-memory columns, rows folded over the 128 lanes) and
 //    their scores and softmax state, so nothing is exchanged between the two
 //    but the cache rows themselves.
-//  * Keys go by in tiles of 64.  Each CTA loads 32 of them, once, with plain
-//    16-byte loads (the next tile's are in flight while this one is stored),
-//    turns e4m3 codes into bf16 exactly, and stores them twice: all 576 dims as
-//    its half of the B operand of the score product (K-major), and the 512
-//    latent dims as rows of the V operand (MN-major), 256 dims here and 256
-//    into the partner's shared memory, since each CTA supplies half the dims of
-//    the aggregation.
+//  * Keys go by in tiles of 64.  A CTA supplies 32 rows of each as its half of the
+//    score product's B operand (576 dims, K-major) and 256 dims of all 64 as its
+//    half of the aggregation's (MN-major).  One warp resolves pool rows and issues
+//    the TMA loads.  bf16 rows (of a prefix: whole pages) land in the operands.
+//    e4m3 rows are gathered four at a time into a two-slot ring; eight warps turn
+//    them into bf16 in registers, exactly, and store them to one-stage operands,
+//    four warps each: the score operand is refilled while the aggregation runs and
+//    the other way round.  Latent dims stand there in the order 0, 2, 1, 3 of each
+//    four (fewer shifts), in the query and the output columns alike.
+//    Measured and dropped: plain loads to registers (the shared memory taken
+//    leaves the L1 too little room for a tile in flight), cp.async (its requests
+//    hold up the barrier arrivals between the CTAs: 2000 cycles per tile), and
+//    sending the rows that the partner aggregates through distributed shared
+//    memory (16 KB per tile at 20 bytes per clock from stores, 10 from bulk copies
+//    and st.async, and a cluster-scope release per tile).
 //  * Four softmax warps: thread = (row, half of the tile's keys).  Online base-2
 //    softmax; the two threads of a row exchange tile maxima through shared
 //    memory, O is rescaled only when a maximum grows by more than 2^8.  P goes
-//    to shared memory as bf16 (the normaliser sums the rounded values, so the
-//    weights applied add up to one; lse uses the fp32 sum).
+//    to shared memory as bf16, as the tensor cores take it (half a step, 2^-8, of
+//    each weight); normaliser and lse use the fp32 values.
 //  * One thread of the even CTA issues scores(t + 1) before aggregation(t).
-//  * A drafted row that holds a non-finite value stays out of V and makes its
-//    scores NaN instead: tokens that see it get NaN, tokens that do not are
-//    untouched (0 * NaN would reach them through the product).
+//  * Drafted rows are masked token by token, so a row that some token must not see
+//    may be in the tile; non-finite contents of such a row are zeroed in the
+//    aggregation operand (0 * NaN would reach every token).  Tokens that see the
+//    row still get NaN, through its scores.
 //  * Few items split their keys over several pairs; partial states go to a
 //    workspace and a combine kernel merges them in split order.
 #include "sa_device.cuh"
@@ -41,26 +50,46 @@ constexpr int kNK = 64;    // keys per tile
 constexpr int kOwn = 32;   // keys of a tile that one CTA loads
 constexpr int kRows = 64;  // query rows per CTA
 constexpr int kQSlice = kRows * 128, kKSlice = kOwn * 128, kVSlice = kNK * 128;  // 64 dims each
-constexpr int kKStage = 9 * kKSlice, kVStage = 4 * kVSlice;
-constexpr int kStages = 2;
-constexpr int kOffQ = 0;
-constexpr int kOffK = kOffQ + 9 * kQSlice;
-constexpr int kOffV = kOffK + kStages * kKStage;
-constexpr int kOffP = kOffV + kStages * kVStage;
-constexpr int kSmem = kOffP + kRows * 128 + 1024;
-constexpr int kORow = 512 * 4 + 16;  // an output row staged in the K and V rings (padded)
-constexpr int kSmxWarps = 4, kProdWarps = 8;
-constexpr int kMmaWarp = kSmxWarps + kProdWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kVStage = 4 * kVSlice;
+constexpr int kSmxWarps = 4, kLoadWarps = 4;  // loading warps of either operand
+constexpr int kKWarp0 = kSmxWarps, kVWarp0 = kKWarp0 + kLoadWarps;
+constexpr int kMmaWarp = kVWarp0 + kLoadWarps;
+constexpr int kTmaWarp = kMmaWarp + 1, kTmaWarps = 3;
+constexpr int kThreads = 32 * (kTmaWarp + kTmaWarps);
+constexpr int kORow = 512 * 4 + 16;  // a staged output row (padded)
+
+// A raw slot (e4m3): this CTA's 32 latent rows of a tile, the partner's, and the
+// scale words of the tile's 64 rows.
+constexpr int kRawOther = kOwn * 512, kRawScale = 2 * kRawOther, kRawSlot = kRawScale + kNK * 4;
+
+template <bool kQ8>
+struct Smem {
+    static constexpr int kStages = kQ8 ? 1 : 2;  // of the latent slices of K, and of V; RoPE slice: two
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + 9 * kQSlice;
+    static constexpr int kOffR = kOffK + kStages * 8 * kKSlice;
+    static constexpr int kOffV = kOffR + 2 * kKSlice;
+    static constexpr int kOffP = kOffV + kStages * kVStage;
+    static constexpr int kOffRaw = kOffP + kRows * 128;
+    static constexpr int kEnd = kOffRaw + (kQ8 ? 2 * kRawSlot : 0);
+    static constexpr int kBytes = kEnd + 1024;
+    static_assert(kOffK % 1024 == 0 && kOffR % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms are 1024-byte aligned");
+    static_assert(kRawSlot % 128 == 0, "TMA destinations are 128-byte aligned");
+    static_assert(kBytes <= 232448 - 3072, "shared memory budget");
+    static_assert(kRows * kORow <= kEnd, "the output rows fit");
+};
+
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;    // two 256-dim products, 128 columns each
 constexpr uint32_t kColS = 256;  // two score buffers of 32 columns
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxSplits = 32;
 
-static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms are 1024-byte aligned");
-static_assert(kSmem <= 232448 - 3072, "shared memory budget");
-static_assert(kRows * kORow <= kStages * (kKStage + kVStage), "the output rows fit in the rings");
+// Tensor maps of the pools.  e4m3: one whole row a box.  bf16: boxes of 64 elements by 32 and by 64 rows,
+// RoPE keys by 32 rows, 128-byte swizzle.
+struct Maps {
+    CUtensorMap c, cv, kr;
+};
 
 struct Args {
     LatentArgs a;
@@ -68,8 +97,32 @@ struct Args {
     int groups;           // items per tree
     int nsplit;
     float* ws_o;   // [item][nsplit][128][512]
-    float* ws_ml;  // [item][nsplit][128][4]: m, l of bf16 P, l of fp32 P
+    float* ws_ml;  // [item][nsplit][128][2]: m, l
 };
+
+// warp_wait that polls without suspending.
+__device__ __forceinline__ bool warp_spin(uint64_t* b, uint32_t parity, const WaitCtx& w, int site) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) {
+        unsigned long long t0 = 0;
+        for (uint32_t n = 0; !mbar_test_wait(b, parity); ++n) {
+            if ((n & 63u) != 63u) continue;
+            if (*w.abort) {
+                ok = 0;
+                break;
+            }
+            const unsigned long long now = global_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > w.limit_ns) {
+                record_error(w.err, site);
+                *w.abort = 1;
+                ok = 0;
+                break;
+            }
+        }
+    }
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
 
 // What one item covers.
 struct Item {
@@ -89,13 +142,60 @@ __device__ __forceinline__ Item item_of(const Args& ka, int item) {
     return it;
 }
 
-__device__ __forceinline__ int latent_row(const LatentArgs& a, int seq, int p) {
-    if (p / kPage >= a.pages_per_seq) return -2;
-    const int64_t at = static_cast<int64_t>(seq) * a.pages_per_seq + p / kPage;
-    const int64_t pg = a.page_table ? a.page_table[at] : at;
-    if (pg < 0 || pg >= a.pool_pages) return -2;
-    return static_cast<int>(pg * kPage + (p % kPage));
+// Pool row of a slot of an item's keys in three steps, each one load that has
+// a while to land: the slot's position (-1: none), the page that holds it, the
+// row.  A broken page table is recorded and row 0 of the pool read instead.
+__device__ __forceinline__ int key_position(const LatentArgs& a, const Item& it, bool in, int slot) {
+    if (!in || slot >= it.n_keys) return -1;
+    return a.idx ? a.idx[static_cast<int64_t>(it.b) * a.k + slot] : slot;
 }
+__device__ __forceinline__ int key_page(const LatentArgs& a, const Item& it, int pos) {
+    if (pos < 0 || pos / kPage >= a.pages_per_seq) return -1;
+    const int64_t at = static_cast<int64_t>(it.seq) * a.pages_per_seq + pos / kPage;
+    return a.page_table ? a.page_table[at] : (at < a.pool_pages ? static_cast<int>(at) : -1);
+}
+__device__ __forceinline__ int key_row(const LatentArgs& a, int pos, int page) {
+    if (pos < 0) return -1;
+    if (page < 0 || page >= a.pool_pages) {
+        record_error(a.err, kErrMlaIndex);
+        return 0;
+    }
+    return page * kPage + (pos % kPage);
+}
+
+// Pool rows and scale words of 32 keys (lane = key) of the tiles to come: the next
+// tile's are known, the one after has its page under way, the third its position.
+template <bool kQ8>
+struct Rows {
+    int row, next, pos2, page2, pos3;
+    uint32_t sc, sc_next;
+
+    __device__ __forceinline__ uint32_t scale_word(const LatentArgs& a, int r) const {
+        return kQ8 && r >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(a.c_scale + r * a.s_ld)) : 0x7F7F7F7Fu;
+    }
+    // slot: the lane's key of tile 0
+    __device__ __forceinline__ void start(const LatentArgs& a, const Item& it, int nt, int slot) {
+        const int p0 = key_position(a, it, 0 < nt, slot), p1 = key_position(a, it, 1 < nt, slot + kNK);
+        pos2 = key_position(a, it, 2 < nt, slot + 2 * kNK);
+        pos3 = key_position(a, it, 3 < nt, slot + 3 * kNK);
+        const int g0 = key_page(a, it, p0), g1 = key_page(a, it, p1);
+        page2 = key_page(a, it, pos2);
+        row = key_row(a, p0, g0);
+        next = key_row(a, p1, g1);
+        sc = scale_word(a, row);
+        sc_next = scale_word(a, next);
+    }
+    // t: the new current tile
+    __device__ __forceinline__ void advance(const LatentArgs& a, const Item& it, int nt, int slot, int t) {
+        row = next;
+        sc = sc_next;
+        next = key_row(a, pos2, page2);
+        sc_next = scale_word(a, next);
+        pos2 = pos3;
+        page2 = key_page(a, it, pos2);
+        pos3 = key_position(a, it, t + 3 < nt, slot + (t + 3) * kNK);
+    }
+};
 
 __device__ __forceinline__ bool bf16x2_bad(uint32_t w) {
     return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
@@ -118,58 +218,51 @@ __device__ __forceinline__ void st_smem_v4(uint32_t addr, uint4 v) {
                  : "memory");
 }
 
-// One tile's rows of a producer warp (4 keys) as loaded: lane l holds 16
-// consecutive dims of an e4m3 row, or 16-byte pieces l and l + 32 of a bf16 row;
-// kr: piece l % 8 of key l / 8.
-template <bool kQ8>
-struct Loaded {
-    uint4 c[4][kQ8 ? 1 : 2];
-    uint32_t sc[kQ8 ? 4 : 1];
-    uint4 kr;
-};
+__device__ __forceinline__ void st_smem_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_smem_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_smem_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
 
-template <bool kQ8>
-__device__ __forceinline__ void load_tile(const LatentArgs& a, int rows4, int lane, Loaded<kQ8>& x) {
-    // rows4: lane i < 4 of each group of 4 lanes holds the pool row of key i (negative: zeros)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = __shfl_sync(0xffffffffu, rows4, i);
-        if (kQ8) {
-            x.c[i][0] = make_uint4(0u, 0u, 0u, 0u);
-            x.sc[i] = 127u;
-            if (row >= 0) {
-                x.c[i][0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.c_cache) + row * a.c_ld) + lane);
-                x.sc[i] = __ldg(a.c_scale + row * a.s_ld + (lane >> 3));
-            }
-        } else {
-#pragma unroll
-            for (int p = 0; p < (kQ8 ? 1 : 2); ++p) {
-                x.c[i][p] = make_uint4(0u, 0u, 0u, 0u);
-                if (row >= 0)
-                    x.c[i][p] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.c_cache) + row * a.c_ld) +
-                                      lane + 32 * p);
-            }
-        }
-    }
-    const int row = __shfl_sync(0xffffffffu, rows4, lane >> 3);
-    x.kr = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= 0)
-        x.kr = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kr_cache) + row * a.kr_ld) + (lane & 7));
+// Sixteen e4m3 dims -> two 16-byte bf16 pieces, each four in the order 0, 2, 1, 3.
+__device__ __forceinline__ void convert16(uint4 u, uint32_t scale, uint4& lo, uint4& hi) {
+    const uint32_t f = q8_scale_bf16x2(scale);
+    const uint2 v0 = e4m3x4_to_bf16x4_0213(u.x, f), v1 = e4m3x4_to_bf16x4_0213(u.y, f);
+    const uint2 v2 = e4m3x4_to_bf16x4_0213(u.z, f), v3 = e4m3x4_to_bf16x4_0213(u.w, f);
+    lo = make_uint4(v0.x, v0.y, v1.x, v1.y);
+    hi = make_uint4(v2.x, v2.y, v3.x, v3.y);
+}
+
+__device__ __forceinline__ bool bad4(uint4 v) {
+    return bf16x2_bad(v.x) | bf16x2_bad(v.y) | bf16x2_bad(v.z) | bf16x2_bad(v.w);
 }
 
 template <bool kQ8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_latent_kernel(const Args ka) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_latent_kernel(const Args ka, const __grid_constant__ Maps maps) {
     pdl_trigger();
+    using S = Smem<kQ8>;
+    constexpr int kStages = S::kStages;
     const LatentArgs& a = ka.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // filled by both CTAs' warps, waited for by the issuing thread (the even CTA's copies are used)
-    __shared__ uint64_t bar_kfull[kStages], bar_vfull[kStages], bar_sfree[2], bar_pfull;
+    __shared__ uint64_t bar_raw[2], bar_rawfree[2];  // e4m3: the ring
+    __shared__ uint64_t bar_kst[2], bar_vst[2];      // loads straight into an operand have landed (e4m3: RoPE slice)
+    // a stage is visible to the tensor cores, the scores are read, P is written: waited for by the
+    // issuing thread (the even CTA's copies are used)
+    __shared__ uint64_t bar_kfull[2], bar_vfull[2], bar_sfree[2], bar_pfull;
     // arrived on in both CTAs when a product is done: scores(t) -> bar_s[t & 1] (K stage free, scores
     // readable), aggregation(t) -> bar_o[t & 1] (V stage and P free, O updated)
     __shared__ uint64_t bar_s[2], bar_o[2], bar_final;
     __shared__ float s_max[2][128];
-    __shared__ float2 s_sum[128];
+    __shared__ float s_sum[128];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ volatile int s_fail[2];
@@ -189,8 +282,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         s_abort = 0;
         s_fail[0] = s_fail[1] = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar_kfull[i], 2 * kProdWarps);
-            mbar_init(&bar_vfull[i], 2 * kProdWarps);
+            mbar_init(&bar_raw[i], 2);
+            mbar_init(&bar_rawfree[i], 2 * kLoadWarps);
+            mbar_init(&bar_kst[i], 1);
+            mbar_init(&bar_vst[i], 1);
+            mbar_init(&bar_kfull[i], kQ8 ? 2 * kLoadWarps : 2);
+            mbar_init(&bar_vfull[i], kQ8 ? 2 * kLoadWarps : 2);
             mbar_init(&bar_sfree[i], 2 * kSmxWarps);
             mbar_init(&bar_s[i], 1);
             mbar_init(&bar_o[i], 1);
@@ -204,42 +301,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         tmem_relinquish_pair();
     }
 
-    // ---- producers: pool rows of the next eight tiles, one (tile, key) per lane
-    const int pw = warp - kSmxWarps;
-    const bool producer = pw >= 0 && pw < kProdWarps;
-    auto resolve = [&](int t) {  // lane l: tile t + l / 4, own key 4 pw + l % 4
-        const int tt = t + (lane >> 2);
-        if (tt >= nt) return -1;
-        const int slot = (t0 + tt) * kNK + static_cast<int>(rank) * kOwn + 4 * pw + (lane & 3);
-        if (slot >= it.n_keys) return -1;
-        const int p = a.idx ? a.idx[static_cast<int64_t>(it.b) * a.k + slot] : slot;
-        if (p < 0) return -1;
-        const int row = latent_row(a, it.seq, p);
-        if (row < 0) record_error(a.err, kErrMlaIndex);
-        return max(row, 0);
-    };
-    int rows8 = -1, rows8_next = -1;
-    Loaded<kQ8> x;
-    if (producer) {
-        rows8 = resolve(0);
-        rows8_next = resolve(8);
-        load_tile<kQ8>(a, rows8, lane, x);
-    }
-
-    // ---- the query rows, as the K-major A operand: row r of this CTA, 16-byte
-    // piece c of its 72 (512 latent dims, then 64 RoPE dims)
-    {
-        uint8_t* sQ = sm + kOffQ;
-        for (int i = tid; i < kRows * 72; i += kThreads) {
-            const int r = i / 72, c = i % 72;
-            const int m = static_cast<int>(rank) * kRows + r;
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (m < it.tokens * a.H) {
-                const int64_t qrow = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + m;
-                v = c < 64 ? __ldg(static_cast<const uint4*>(a.q_lat) + qrow * 64 + c)
-                           : __ldg(static_cast<const uint4*>(a.q_rope) + qrow * 8 + (c - 64));
+    const uint32_t kbase = smem_u32(sm + S::kOffK), vbase = smem_u32(sm + S::kOffV), raw = smem_u32(sm + S::kOffRaw);
+    const int own0 = static_cast<int>(rank) * kOwn, other0 = kOwn - own0;  // this CTA's keys of a tile, the partner's
+    // TMA warps.  e4m3: one for the latent rows of this CTA's keys of a tile, one for the partner's, one
+    // for the RoPE rows (a warp issues a four-row gather every 80 cycles, whatever the rows' size).
+    // bf16: the first loads whole tiles.
+    const int tw = warp - kTmaWarp;
+    const int key0 = kQ8 ? (tw == 1 ? other0 : own0) : 0;
+    Rows<kQ8> keys;
+    if (warp >= kTmaWarp) {
+        if (lane == 0) {
+            tma_prefetch_desc(&maps.c);
+            if (!kQ8) tma_prefetch_desc(&maps.cv);
+            tma_prefetch_desc(&maps.kr);
+        }
+        if (kQ8 || tw == 0) keys.start(a, it, nt, t0 * kNK + key0 + lane);
+    } else {
+        // the query rows, as the K-major A operand: row r of this CTA, 16-byte piece c of its 72
+        // (512 latent dims, then 64 RoPE dims); rows that are not live are zero
+        const uint32_t sQ = smem_u32(sm + S::kOffQ);
+        const int rows = it.tokens * a.H - static_cast<int>(rank) * kRows;
+        const int64_t q0 = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + rank * kRows;
+        constexpr int kQThreads = 32 * kTmaWarp, kFlight = 6;
+#pragma unroll 1
+        for (int i0 = tid; i0 < kRows * 72; i0 += kFlight * kQThreads) {
+            uint4 v[kFlight];
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+                const int i = i0 + k * kQThreads, r = i / 72, c = i % 72;
+                const bool in = i < kRows * 72 && r < rows;
+                const uint4* src = c < 64 ? static_cast<const uint4*>(a.q_lat) + (q0 + r) * 64 + c
+                                          : static_cast<const uint4*>(a.q_rope) + (q0 + r) * 8 + (c - 64);
+                v[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (in) v[k] = __ldg(src);
             }
-            *reinterpret_cast<uint4*>(sQ + (c >> 3) * kQSlice + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+                const int i = i0 + k * kQThreads, r = i / 72, c = i % 72;
+                if (kQ8 && c < 64)
+                    v[k] = make_uint4(__byte_perm(v[k].x, v[k].y, 0x5410), __byte_perm(v[k].x, v[k].y, 0x7632),
+                                      __byte_perm(v[k].z, v[k].w, 0x5410), __byte_perm(v[k].z, v[k].w, 0x7632));
+                if (i < kRows * 72) st_smem_v4(sQ + (c >> 3) * kQSlice + r * 128 + (((c & 7) ^ (r & 7)) << 4), v[k]);
+            }
         }
         fence_proxy_async_smem();
     }
@@ -249,149 +352,223 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     tc_fence_after();
     const uint32_t tmem = s_tmem;
 
-    if (nt == 0) {
+    if (nt <= 0) {
         // no keys: fall through (the softmax warps write the empty result)
-    } else if (producer) {
-        const uint32_t kfull0 = mapa_u32(smem_u32(&bar_kfull[0]), 0), vfull0 = mapa_u32(smem_u32(&bar_vfull[0]), 0);
-        // this lane's dim slices and where their V copy goes: slice s (64 dims)
-        // belongs to CTA (s % 4) / 2, as its slice 2 (s / 4) + s % 2
-        constexpr int kPieces = 2;  // 16-byte bf16 pieces per row and lane
-        uint32_t koff[kPieces], voff[kPieces];
-        const uint32_t vb[2] = {mapa_u32(smem_u32(sm + kOffV), 0), mapa_u32(smem_u32(sm + kOffV), 1)};
-        int chunk[kPieces];
+    } else if (warp >= kTmaWarp) {
+        // ------------------------------------------ loads
+        int issued = 0, issued_v = 0;
+        if (kQ8) {
+            for (int t = 0; t < nt; ++t) {
+                const int st = t & 1;
+                // the slot has been read; the RoPE slice's products are done
+                if (t >= 2 && !warp_wait(tw == 2 ? &bar_s[st] : &bar_rawfree[st], static_cast<uint32_t>((t >> 1) & 1) ^ 1, wc,
+                                         kErrLatWait | 1))
+                    break;
+                uint64_t* landed = tw == 2 ? &bar_kst[st] : &bar_raw[st];
+                const uint32_t bar = smem_u32(landed);
+                const uint32_t dst = tw == 2 ? smem_u32(sm + S::kOffR) + st * kKSlice : raw + st * kRawSlot + tw * kRawOther;
+                const int bytes = tw == 2 ? 128 : 512;  // per row
+                const CUtensorMap* map = tw == 2 ? &maps.kr : &maps.c;
+                if (tw < 2) st_smem_u32(raw + st * kRawSlot + kRawScale + 4 * (key0 + lane), keys.sc);
+                __syncwarp();
+                if (elect_one()) mbar_arrive_expect_tx(landed, kOwn * bytes);
+                __syncwarp();
+                // (under elect_one: from divergent lanes the issue is slower)
 #pragma unroll
-        for (int p = 0; p < kPieces; ++p) {
-            // e4m3: dims 16 lane ..: pieces 2 lane, 2 lane + 1 (odd slices store theirs in the other
-            // order, so that the eight lanes of a store phase touch distinct banks); bf16: lane, lane + 32
-            const int c = kQ8 ? 2 * lane + (p ^ ((lane >> 2) & 1)) : lane + 32 * p;
-            const int s = c >> 3;
-            chunk[p] = c & 7;
-            koff[p] = smem_u32(sm + kOffK) + s * kKSlice;
-            voff[p] = vb[(s & 3) >> 1] + (2 * (s >> 2) + (s & 1)) * kVSlice;
+                for (int g = 0; g < 8; ++g) {
+                    int r[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(0xffffffffu, keys.row, 4 * g + i);
+                    if (elect_one()) tma_gather4(dst + 4 * g * bytes, map, bar, 0, r[0], r[1], r[2], r[3]);
+                    __syncwarp();
+                }
+                issued = t + 1;
+                keys.advance(a, it, nt, t0 * kNK + key0 + lane, t + 1);
+            }
+        } else if (tw == 0) {
+            // A tile is one page: the row of the tile's key 0 (keys past the last one are masked, and
+            // cleaned in the aggregation operand).  The score operand of a tile comes before the
+            // aggregation operand of the tile before it, as their stages become free.
+            int row0 = 0;
+            for (int t = 0; t <= nt; ++t) {
+                const uint32_t par = static_cast<uint32_t>((t >> 1) & 1) ^ 1;  // tile t - 2's products
+                const int row1 = row0, st = t & 1;
+                if (t < nt) {
+                    row0 = __shfl_sync(0xffffffffu, keys.row, 0);
+                    if (t >= 2 && !warp_wait(&bar_s[st], par, wc, kErrLatWait | 1)) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&bar_kst[st], 9 * kKSlice);
+                        for (int sl = 0; sl < 8; ++sl)
+                            tma_load_2d(sm + S::kOffK + (8 * st + sl) * kKSlice, &maps.c, &bar_kst[st], 64 * sl, row0 + own0);
+                        tma_load_2d(sm + S::kOffR + st * kKSlice, &maps.kr, &bar_kst[st], 0, row0 + own0);
+                    }
+                    __syncwarp();
+                    issued = t + 1;
+                    keys.advance(a, it, nt, t0 * kNK + lane, t + 1);
+                }
+                if (t >= 1) {
+                    const int u = t - 1, vs = u & 1;
+                    if (u >= 2 && !warp_wait(&bar_o[vs], static_cast<uint32_t>((u >> 1) & 1) ^ 1, wc, kErrLatWait | 2)) break;
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&bar_vst[vs], kVStage);
+                        for (int sl = 0; sl < 4; ++sl)
+                            tma_load_2d(sm + S::kOffV + vs * kVStage + sl * kVSlice, &maps.cv, &bar_vst[vs],
+                                        256 * (sl >> 1) + 128 * static_cast<int>(rank) + 64 * (sl & 1), row1);
+                    }
+                    __syncwarp();
+                    issued_v = t;
+                }
+            }
         }
-        const uint32_t kroff = smem_u32(sm + kOffK) + 8 * kKSlice;
-        for (int t = 0; t < nt; ++t) {
-            const int st = t & 1;
-            const uint32_t par = static_cast<uint32_t>(((t >> 1) & 1) ^ 1);
-            // bf16 pieces of this tile
-            uint4 w[4][kPieces];
-            uint4 kr = x.kr;
+        // every load has landed (fixed limit) before the CTA can exit
+        if (lane == 0) {
+            int dummy = 0;
+            WaitCtx dw(a.err, reinterpret_cast<volatile int*>(&dummy), kWaitLimitNs);
+            for (int t = max(0, issued - 2); t < issued; ++t)
+                mbar_wait(kQ8 && tw < 2 ? &bar_raw[t & 1] : &bar_kst[t & 1], static_cast<uint32_t>(t >> 1 & 1), dw, kErrLatWait | 14);
+            for (int t = max(0, issued_v - 2); t < issued_v; ++t)
+                mbar_wait(&bar_vst[t & 1], static_cast<uint32_t>(t >> 1 & 1), dw, kErrLatWait | 15);
+        }
+        __syncwarp();
+    } else if (kQ8 && warp >= kKWarp0 && warp < kMmaWarp) {
+        // ------------------------------------------ e4m3 rows into an operand.  Unit i of a warp: 16 dims
+        // per lane of row i (scores: own row 8 lw + i) or of rows i and 8 + i (aggregation: rows 16 lw + ..
+        // of the tile, lanes 16 .. 31 the second).  One code for both: they differ in what a lane's
+        // pieces start from.
+        const bool v = warp >= kVWarp0;
+        const int lw = warp - (v ? kVWarp0 : kKWarp0);
+        const int vrow = 16 * lw + 8 * (lane >> 4);             // aggregation: the lane's row of unit 0
+        const bool from_own = !v || (vrow & kOwn) == own0;      // (warp-uniform)
+        const int q = v ? vrow & (kOwn - 1) : 8 * lw;           // its index among those 32 rows
+        const int blk = lane >> 3 & 1;
+        // where the lane's 16 bytes of unit 0 stand in the slot
+        const uint32_t src0 = raw + (from_own ? 0 : kRawOther) + q * 512 +
+                              (v ? 256 * blk + 128 * rank + 16 * (lane & 7) : 16 * lane);
+        const uint32_t sc0 = raw + kRawScale + 4 * (v ? vrow + (lane & 7) : own0 + 8 * lw + (lane & 7));  // scale word of unit lane % 8
+        const int sc_shift = v ? 16 * blk + 8 * static_cast<int>(rank) : lane & 24;
+        // pieces c, c ^ 1 of slice lane / 4; odd slices store theirs in the other order, so that the
+        // eight lanes of a store phase touch distinct banks
+        const bool odd = lane >> 2 & 1;
+        const uint32_t c = 2 * (lane & 3) + (odd ? 1 : 0);
+        const uint32_t dst0 = v ? vbase + (lane >> 2 & 3) * kVSlice + vrow * 128 : kbase + (lane >> 2) * kKSlice + 8 * lw * 128;
+        uint64_t* freed = v ? bar_o : bar_s;
+        const uint32_t full = mapa_u32(smem_u32(v ? &bar_vfull[0] : &bar_kfull[0]), 0);
+        uint4 u[8];
+        uint32_t sc = 0;
+        auto fetch = [&](int t) {
+            if (!warp_wait(&bar_raw[t & 1], static_cast<uint32_t>(t >> 1 & 1), wc, kErrLatWait | 13)) return false;
+            const uint32_t slot = (t & 1) * kRawSlot;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (kQ8) {
-                    const uint32_t s2 = q8_scale_bf16x2(x.sc[i]);
-                    const uint2 a0 = e4m3x4_to_bf16x4(x.c[i][0].x, s2), a1 = e4m3x4_to_bf16x4(x.c[i][0].y, s2);
-                    const uint2 a2 = e4m3x4_to_bf16x4(x.c[i][0].z, s2), a3 = e4m3x4_to_bf16x4(x.c[i][0].w, s2);
-                    const uint4 lo = make_uint4(a0.x, a0.y, a1.x, a1.y), hi = make_uint4(a2.x, a2.y, a3.x, a3.y);
-                    const bool odd = (lane >> 2) & 1;
-                    w[i][0] = odd ? hi : lo;
-                    w[i][1] = odd ? lo : hi;
-                } else {
+            for (int i = 0; i < 8; ++i) u[i] = ld_smem_v4(src0 + slot + i * 512);
+            sc = ld_smem_u32(sc0 + slot);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_rawfree[t & 1]);
+            return true;
+        };
+        bool ok = fetch(0);
+        for (int t = 0; ok && t < nt; ++t) {
+            uint4 w[8][2];
 #pragma unroll
-                    for (int p = 0; p < kPieces; ++p) w[i][p] = x.c[i][kQ8 ? 0 : p];
-                }
+            for (int i = 0; i < 8; ++i) {
+                uint4 lo, hi;
+                convert16(u[i], __shfl_sync(0xffffffffu, sc, (lane & 16) + i) >> sc_shift & 255u, lo, hi);
+                w[i][0] = odd ? hi : lo;
+                w[i][1] = odd ? lo : hi;
             }
-            // the next tile's loads
-            if (t + 1 < nt) {
-                const int u = (t + 1) & 7;
-                if (u == 0) {
-                    rows8 = rows8_next;
-                    rows8_next = resolve(t + 9);
-                }
-                load_tile<kQ8>(a, __shfl_sync(0xffffffffu, rows8, 4 * u + (lane & 3)), lane, x);
+            // the next tile's codes, before the wait for the operand: the slot is free that much earlier
+            if (t + 1 < nt && !fetch(t + 1)) break;
+            const int tile0 = (t0 + t) * kNK;
+            if (v && a.tree && tile0 + kNK > it.past) {  // drafted rows: non-finite contents stay out of the aggregation
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (tile0 + vrow + i >= it.past && (bad4(w[i][0]) || bad4(w[i][1]))) w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
             }
-            // drafted rows with non-finite contents: out of V, NaN in K
-            uint32_t bad = 0;
-            const int own0 = (t0 + t) * kNK + static_cast<int>(rank) * kOwn + 4 * pw;  // this warp's first slot
-            if (a.tree && own0 + 3 >= it.past) {
-                const uint32_t kb = __ballot_sync(0xffffffffu, bf16x2_bad(kr.x) | bf16x2_bad(kr.y) | bf16x2_bad(kr.z) |
-                                                                   bf16x2_bad(kr.w));
+            if (t >= 1 && !warp_wait(&freed[(t - 1) & 1], static_cast<uint32_t>(t - 1 >> 1 & 1), wc, kErrLatWait | 2)) break;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    bool any = (kb >> (8 * i) & 0xFFu) != 0;
-#pragma unroll
-                    for (int p = 0; p < kPieces; ++p)
-                        any |= bf16x2_bad(w[i][p].x) | bf16x2_bad(w[i][p].y) | bf16x2_bad(w[i][p].z) | bf16x2_bad(w[i][p].w);
-                    if (__any_sync(0xffffffffu, any) && own0 + i >= it.past) bad |= 1u << i;
-                }
-                if (bad >> (lane >> 3) & 1u) kr = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-            }
-            if (t >= kStages && !warp_wait(&bar_s[st], par, wc, kErrLatWait | 1)) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = 4 * pw + i;
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p)
-                    st_smem_v4(koff[p] + st * kKStage + j * 128 + ((chunk[p] ^ (j & 7)) << 4), w[i][p]);
-            }
-            {
-                const int j = 4 * pw + (lane >> 3);
-                st_smem_v4(kroff + st * kKStage + j * 128 + (((lane & 7) ^ (j & 7)) << 4), kr);
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t off = i * 128 + ((c ^ i) << 4);
+                st_smem_v4(dst0 + off, w[i][0]);
+                st_smem_v4(dst0 + (off ^ 16), w[i][1]);
             }
             fence_proxy_async_smem();
+            // one warp's report covers the RoPE slice
+            if (!v && lw == 0 && !warp_wait(&bar_kst[t & 1], static_cast<uint32_t>(t >> 1 & 1), wc, kErrLatWait | 3)) break;
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(kfull0 + 8 * st);
-            if (t >= kStages && !warp_wait(&bar_o[st], par, wc, kErrLatWait | 2)) break;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = static_cast<int>(rank) * kOwn + 4 * pw + i;
-                if (bad >> i & 1u) w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int p = 0; p < kPieces; ++p)
-                    st_cluster_v4(voff[p] + st * kVStage + j * 128 + ((chunk[p] ^ (j & 7)) << 4), w[i][p].x, w[i][p].y,
-                                  w[i][p].z, w[i][p].w);
-            }
-            fence_proxy_async_cluster();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(vfull0 + 8 * st);
+            if (lane == 0) mbar_arrive_remote(full);
         }
+    } else if (!kQ8 && (warp == kKWarp0 || warp == kVWarp0)) {
+        // ------------------------------------------ bf16 operands reported (and cleaned)
+        const bool v = warp == kVWarp0;
+        uint64_t* landed = v ? bar_vst : bar_kst;
+        const uint32_t full = mapa_u32(smem_u32(v ? &bar_vfull[0] : &bar_kfull[0]), 0);
+        for (int t = 0; t < nt; ++t) {
+            const int st = t & 1;
+            if (!warp_wait(&landed[st], static_cast<uint32_t>(t >> 1 & 1), wc, kErrLatWait | 13)) break;
+            const int tile0 = (t0 + t) * kNK;
+            if (v && tile0 + kNK > it.past) {  // lane = 16-byte piece of a row
+                for (int j = max(0, it.past - tile0); j < kNK; ++j) {
+                    const uint32_t at = vbase + st * kVStage + (lane >> 3) * kVSlice + j * 128 + (((lane & 7) ^ (j & 7)) << 4);
+                    if (bad4(ld_smem_v4(at))) st_smem_v4(at, make_uint4(0u, 0u, 0u, 0u));
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_remote(full + 8 * st);
+        }
+        __syncwarp();
     } else if (warp == kMmaWarp) {
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             constexpr uint32_t id_qk = idesc_f32acc(1, 1, false, false, 128, kNK);
             constexpr uint32_t id_pv = idesc_f32acc(1, 1, false, true, 128, 256);
+            const uint64_t qd = sdesc(smem_u32(sm + S::kOffQ), 16, 1024, kSw128);
+            const uint64_t kd0 = sdesc(smem_u32(sm + S::kOffK), 16, 1024, kSw128);
+            const uint64_t rd0 = sdesc(smem_u32(sm + S::kOffR), 16, 1024, kSw128);
+            const uint64_t pd = sdesc(smem_u32(sm + S::kOffP), 16, 1024, kSw128);
+            const uint64_t vd0 = sdesc(smem_u32(sm + S::kOffV), kVSlice, 1024, kSw128);
             bool ok = true;
-            for (int t = 0; ok && t <= nt; ++t) {
+            for (int t = 0; t <= nt; ++t) {
                 if (t < nt) {  // scores(t)
-                    const int st = t & 1;
-                    const uint32_t ph = static_cast<uint32_t>((t >> 1) & 1);
-                    ok = mbar_wait<true>(&bar_kfull[st], ph, wc, kErrLatWait | 3) &&
-                         (t < 2 || mbar_wait<true>(&bar_sfree[st], ph ^ 1, wc, kErrLatWait | 4));
+                    const int st = t % kStages, sb = t & 1;
+                    ok = warp_spin(&bar_kfull[st], static_cast<uint32_t>(t / kStages & 1), wc, kErrLatWait | 3) &&
+                         (t < 2 || warp_spin(&bar_sfree[sb], static_cast<uint32_t>(t >> 1 & 1) ^ 1, wc, kErrLatWait | 4));
                     if (!ok) break;
-                    fence_proxy_async_cluster();
                     tc_fence_after();
-                    for (int bb = 0; bb < 9; ++bb) {
-                        const uint64_t qd = sdesc(smem_u32(sm + kOffQ + bb * kQSlice), 16, 1024, kSw128);
-                        const uint64_t kd = sdesc(smem_u32(sm + kOffK + st * kKStage + bb * kKSlice), 16, 1024, kSw128);
+                    const uint64_t kd = kd0 + static_cast<uint32_t>(st * (8 * kKSlice >> 4));
+                    const uint64_t rd = rd0 + static_cast<uint32_t>(sb * (kKSlice >> 4));
+                    const uint32_t sc = tmem + kColS + 32 * sb;
+                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_bf16_pair(tmem + kColS + 32 * st, qd + 2 * kk, kd + 2 * kk, id_qk, (bb | kk) != 0 ? 1u : 0u);
+                        for (int i = 0; i < 36; ++i)  // 64-dim slice i / 4, 16 dims each
+                            mma_bf16_pair(sc, qd + (i >> 2) * (kQSlice >> 4) + 2 * (i & 3),
+                                          (i < 32 ? kd + (i >> 2) * (kKSlice >> 4) : rd) + 2 * (i & 3), id_qk, i != 0 ? 1u : 0u);
+                        tc_commit_pair(&bar_s[sb]);
                     }
-                    tc_commit_pair(&bar_s[st]);
+                    __syncwarp();
                 }
                 if (t > 0) {  // aggregation(t - 1)
-                    const int u = t - 1, st = u & 1;
-                    ok = mbar_wait<true>(&bar_vfull[st], static_cast<uint32_t>((u >> 1) & 1), wc, kErrLatWait | 5) &&
-                         mbar_wait<true>(&bar_pfull, static_cast<uint32_t>(u & 1), wc, kErrLatWait | 6);
+                    const int u = t - 1, st = u % kStages;
+                    ok = warp_spin(&bar_vfull[st], static_cast<uint32_t>(u / kStages & 1), wc, kErrLatWait | 5) &&
+                         warp_spin(&bar_pfull, static_cast<uint32_t>(u & 1), wc, kErrLatWait | 6);
                     if (!ok) break;
-                    fence_proxy_async_cluster();
                     tc_fence_after();
-                    const uint64_t pd = sdesc(smem_u32(sm + kOffP), 16, 1024, kSw128);
+                    const uint64_t vd = vd0 + static_cast<uint32_t>(st * (kVStage >> 4));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint64_t vd = sdesc(smem_u32(sm + kOffV + st * kVStage + 2 * j * kVSlice), kVSlice, 1024, kSw128);
-#pragma unroll
-                        for (int kk = 0; kk < kNK / 16; ++kk)
-                            mma_bf16_pair(tmem + kColO + 128 * j, pd + 2 * kk, vd + 128 * kk, id_pv,
-                                          (u > 0 || kk > 0) ? 1u : 0u);
+                        for (int i = 0; i < 8; ++i)  // 256 dims i / 4, 16 keys each
+                            mma_bf16_pair(tmem + kColO + 128 * (i >> 2), pd + 2 * (i & 3),
+                                          vd + (i >> 2) * (2 * kVSlice >> 4) + 128 * (i & 3), id_pv,
+                                          u > 0 || (i & 3) != 0 ? 1u : 0u);
+                        tc_commit_pair(&bar_o[u & 1]);
                     }
-                    tc_commit_pair(&bar_o[st]);
+                    __syncwarp();
                 }
             }
             // every product has finished (fixed limit) before the pair tears down
             int dummy = 0;
             WaitCtx dw(a.err, reinterpret_cast<volatile int*>(&dummy), kWaitLimitNs);
-            tc_commit_pair(&bar_final);
-            mbar_wait(&bar_final, 0, dw, kErrLatWait | 7);
+            if (elect_one()) tc_commit_pair(&bar_final);
+            __syncwarp();
+            if (lane == 0) mbar_wait(&bar_final, 0, dw, kErrLatWait | 7);
         } else if (lane == 0) {
             // the last arrival this CTA gets (the even CTA's waits all have limits, so it comes)
             int dummy = 0;
@@ -408,16 +585,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         const int token = it.i0 + (live ? m_row / a.H : 0);
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t sfree0 = mapa_u32(smem_u32(&bar_sfree[0]), 0), pfull0 = mapa_u32(smem_u32(&bar_pfull), 0);
-        const uint32_t prow = smem_u32(sm + kOffP) + r * 128;
+        const uint32_t prow = smem_u32(sm + S::kOffP) + r * 128;
         const float c2 = a.scale * 1.4426950408889634f;  // scores in base-2 units
-        float m = -INFINITY, l = 0.f, lx = 0.f;
+        float m = -INFINITY, l = 0.f;
         bool ok = true;
-        // which of this thread's 32 keys of tile t it attends to
+        // which of this thread's 32 keys of tile t it attends to.  Selections: the
+        // slots of eight tiles are loaded eight tiles ahead (the fence that
+        // publishes P waits for loads in flight); lane u holds tile u's mask.
+        int slots[8];
+        uint32_t vis8 = 0;
+        auto load_slots = [&](int t) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int s = (t0 + t + u) * kNK + hf * 32 + lane;
+                slots[u] = t + u < nt && s < a.k ? a.idx[static_cast<int64_t>(it.b) * a.k + s] : -1;
+            }
+        };
+        auto next_slots = [&](int t) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const uint32_t v = __ballot_sync(0xffffffffu, slots[u] >= 0);
+                if (lane == u) vis8 = v;
+            }
+            load_slots(t + 8);
+        };
         auto visible = [&](int t) -> uint32_t {
             const int s0 = (t0 + t) * kNK + hf * 32;
             if (a.idx) {
-                const int s = s0 + lane;
-                return __ballot_sync(0xffffffffu, s < a.k && a.idx[static_cast<int64_t>(it.b) * a.k + s] >= 0);
+                if ((t & 7) == 0) next_slots(t);
+                return __shfl_sync(0xffffffffu, vis8, t & 7);
             }
             if (s0 + 32 <= it.past) return 0xffffffffu;
             uint32_t v = s0 < it.past ? (1u << (it.past - s0)) - 1u : 0u;
@@ -429,6 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             }
             return v;
         };
+        if (a.idx) load_slots(0);
         uint32_t vis = nt > 0 ? visible(0) : 0u;
         for (int t = 0; t < nt; ++t) {
             const int sb = t & 1;
@@ -441,9 +638,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(sfree0 + 8 * sb);
+                if (lane == 0) mbar_arrive_cluster_relaxed(sfree0 + 8 * sb);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = (vis >> j & 1u) ? __uint_as_float(v[j]) * c2 : -INFINITY;
+                for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j]) * c2;
+                if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!(vis >> j & 1u)) s[j] = -INFINITY;
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) s[j] = -INFINITY;
@@ -465,7 +667,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 const float m_new = grow ? top : m;
                 const float alpha = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - m_new)) : 1.f;
                 if (t > 0) {  // O holds the tiles before t
-                    ok = warp_wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>(((t - 1) >> 1) & 1), wc, kErrLatWait | 9);
+                    ok = warp_wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), wc, kErrLatWait | 9);
                     if (ok) {
                         tc_fence_after();
 #pragma unroll 1
@@ -481,25 +683,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     }
                 }
                 l *= alpha;
-                lx *= alpha;
                 m = m_new;
             }
             const float mref = m == -INFINITY ? 0.f : m;  // masked keys are -inf and give exactly 0
             uint32_t pk[16];
-            float lb = 0.f, lf = 0.f;
+            float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float p0 = fast_exp2(s[2 * j] - mref), p1 = fast_exp2(s[2 * j + 1] - mref);
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-                lb += __low2float(b2) + __high2float(b2);
-                lf += p0 + p1;
-                pk[j] = *reinterpret_cast<const uint32_t*>(&b2);
+                sum += p0 + p1;
+                pk[j] = pack_bf16x2(p0, p1);
             }
-            l += lb;
-            lx += lf;
+            l += sum;
             // aggregation(t - 1) has read P
             if (ok && t > 0)
-                ok = warp_wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>(((t - 1) >> 1) & 1), wc, kErrLatWait | 10);
+                ok = warp_wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), wc, kErrLatWait | 10);
             if (ok) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -508,24 +706,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(pfull0);
+                if (lane == 0) mbar_arrive_remote(pfull0);
             }
         }
-        // ---- both halves' sums, then the rows out: staged in the idle rings, bulk copies
-        s_sum[tid] = make_float2(l, lx);
+        // ---- both halves' sums, then the rows out: staged over the idle operands, bulk copies
+        s_sum[tid] = l;
         named_sync(1, 32 * kSmxWarps);
-        l += s_sum[tid ^ 64].x;
-        lx += s_sum[tid ^ 64].y;
+        l += s_sum[tid ^ 64];
         if (ok && nt > 0)
-            ok = warp_wait(&bar_o[(nt - 1) & 1], static_cast<uint32_t>(((nt - 1) >> 1) & 1), wc, kErrLatWait | 11);
+            ok = warp_wait(&bar_o[(nt - 1) & 1], static_cast<uint32_t>((nt - 1) >> 1 & 1), wc, kErrLatWait | 11);
         if (ok && !*wc.abort) {
             tc_fence_after();
             const bool partial = ka.nsplit > 1;
             const bool bf = !partial && a.out_bf16 != nullptr;
             const bool empty = l == 0.f;  // (a NaN sum is not empty)
             const float inv = empty || partial ? 1.f : 1.f / l;
-            uint8_t* srow = sm + kOffK + r * kORow;
-            const int e = bf ? 2 : 4;
+            uint8_t* srow = sm + r * kORow;
 #pragma unroll 1
             for (int c = 0; c < 256; c += 32) {
                 const int d = (c >> 7) * 256 + hf * 128 + (c & 127);
@@ -538,7 +734,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 for (int j = 0; j < 32; j += 4) {
                     float f[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = empty ? 0.f : __uint_as_float(o[j + i]) * inv;
+                    for (int i = 0; i < 4; ++i) {
+                        const int n = kQ8 && (i == 1 || i == 2) ? 3 - i : i;  // dims in the order 0, 2, 1, 3
+                        f[i] = empty ? 0.f : __uint_as_float(o[j + n]) * inv;
+                    }
                     if (bf)
                         *reinterpret_cast<uint2*>(srow + 2 * (d + j)) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
                     else
@@ -546,26 +745,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 }
             }
             fence_proxy_async_smem();
-            if (live) {
-                const int64_t orow = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + m_row;
-                const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
-                uint8_t* dst = partial ? reinterpret_cast<uint8_t*>(ka.ws_o + wrow * 512)
-                                       : (bf ? static_cast<uint8_t*>(a.out_bf16) + orow * 1024
-                                             : reinterpret_cast<uint8_t*>(a.out + orow * 512));
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int d = j * 256 + hf * 128;
-                    bulk_copy_s2g(dst + d * e, srow + d * e, 128 * e);
-                }
-                if (hf == 0) {
-                    if (partial) {
-                        *reinterpret_cast<float4*>(ka.ws_ml + wrow * 4) = make_float4(m, l, lx, 0.f);
-                    } else if (a.lse) {
-                        a.lse[orow] = empty ? -INFINITY : (m + log2f(lx)) * 0.6931471805599453f;
-                    }
-                }
-                bulk_wait_all();
-            }
+        }
+        named_sync(1, 32 * kSmxWarps);  // both threads of a row have staged it (one bulk copy per row)
+        if (ok && !*wc.abort && live && hf == 0) {
+            const bool partial = ka.nsplit > 1;
+            const int64_t orow = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + m_row;
+            const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
+            uint8_t* dst = partial ? reinterpret_cast<uint8_t*>(ka.ws_o + wrow * 512)
+                                   : (a.out_bf16 ? static_cast<uint8_t*>(a.out_bf16) + orow * 1024
+                                                 : reinterpret_cast<uint8_t*>(a.out + orow * 512));
+            bulk_copy_s2g(dst, sm + r * kORow, !partial && a.out_bf16 ? 1024 : 2048);
+            if (partial)
+                *reinterpret_cast<float2*>(ka.ws_ml + wrow * 2) = make_float2(m, l);
+            else if (a.lse)
+                a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            bulk_wait_all();
         }
     }
 
@@ -592,21 +786,18 @@ __global__ void __launch_bounds__(kCombThreads) mla_latent_combine_kernel(const 
     const int item = b * ka.groups + token / ka.tokens_per_item;
     const int64_t w0 = static_cast<int64_t>(item) * ka.nsplit * 128 + token % ka.tokens_per_item * a.H + h;
     // lane s holds split s's state
-    float ms = -INFINITY, ls = 0.f, xs = 0.f;
+    float ms = -INFINITY, ls = 0.f;
     if (lane < ka.nsplit) {
-        const float4 v = *reinterpret_cast<const float4*>(ka.ws_ml + (w0 + static_cast<int64_t>(lane) * 128) * 4);
-        ms = v.x, ls = v.y, xs = v.z;
+        const float2 v = *reinterpret_cast<const float2*>(ka.ws_ml + (w0 + static_cast<int64_t>(lane) * 128) * 2);
+        ms = v.x, ls = v.y;
     }
     float top = ls != 0.f ? ms : -INFINITY;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float wgt = ls != 0.f ? exp2f(ms - top) : 0.f;
-    float L = ls * wgt, LX = xs * wgt;
+    float L = ls * wgt;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        L += __shfl_xor_sync(0xffffffffu, L, o);
-        LX += __shfl_xor_sync(0xffffffffu, LX, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     float4 acc[4];
 #pragma unroll
     for (int p = 0; p < 4; ++p) acc[p] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -630,7 +821,7 @@ __global__ void __launch_bounds__(kCombThreads) mla_latent_combine_kernel(const 
         else
             *reinterpret_cast<float4*>(a.out + orow * 512 + 128 * p + 4 * lane) = make_float4(x, y, z, w);
     }
-    if (a.lse && lane == 0) a.lse[orow] = L == 0.f ? -INFINITY : (top + log2f(LX)) * 0.6931471805599453f;
+    if (a.lse && lane == 0) a.lse[orow] = L == 0.f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
 }
 
 int tokens_per_item(int T, int H) {
@@ -649,14 +840,27 @@ int splits(int64_t items, int k) {
     return ns < 1 ? 1 : static_cast<int>(ns);
 }
 
-size_t state_bytes(int64_t items, int ns) { return static_cast<size_t>(items) * ns * 128 * (512 + 4) * 4; }
+size_t state_bytes(int64_t items, int ns) { return static_cast<size_t>(items) * ns * 128 * (512 + 2) * 4; }
 
 template <bool kQ8>
-cudaError_t launch(const Args& ka, int64_t items, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(mla_latent_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    mla_latent_kernel<kQ8><<<static_cast<unsigned>(2 * items * ka.nsplit), kThreads, kSmem, st>>>(ka);
-    return cudaGetLastError();
+sa_status launch(const Args& ka, int64_t items, cudaStream_t st) {
+    const LatentArgs& a = ka.a;
+    const uint64_t rows = static_cast<uint64_t>(a.pool_pages) * kPage;
+    Maps maps = {};
+    const uint64_t dims[2] = {kQ8 ? 256u : 512u, rows}, rdims[2] = {64, rows};  // (e4m3: pairs of codes)
+    const uint64_t stride[1] = {static_cast<uint64_t>(a.c_ld) * (kQ8 ? 1 : 2)}, rstride[1] = {static_cast<uint64_t>(a.kr_ld) * 2};
+    const uint32_t box[2] = {kQ8 ? 256u : 64u, kQ8 ? 1u : 32u}, vbox[2] = {64u, 64u};
+    const uint32_t rbox[2] = {64u, kQ8 ? 1u : 32u};
+    const CUtensorMapDataType dt = kQ8 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle swz = kQ8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;  // of latent rows
+    if (!encode_tiled(&maps.c, dt, 2, a.c_cache, dims, stride, box, swz) ||
+        (!kQ8 && !encode_tiled(&maps.cv, dt, 2, a.c_cache, dims, stride, vbox, swz)) ||
+        !encode_tiled(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kr_cache, rdims, rstride, rbox, CU_TENSOR_MAP_SWIZZLE_128B))
+        return SA_ECUDA;
+    const cudaError_t e = cudaFuncSetAttribute(mla_latent_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kQ8>::kBytes);
+    if (e != cudaSuccess) return launch_status(e);
+    mla_latent_kernel<kQ8><<<static_cast<unsigned>(2 * items * ka.nsplit), kThreads, Smem<kQ8>::kBytes, st>>>(ka, maps);
+    return launch_status(cudaGetLastError());
 }
 
 }  // namespace
@@ -680,14 +884,14 @@ sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cuda
         ka.ws_o = static_cast<float*>(ws);
         ka.ws_ml = ka.ws_o + static_cast<size_t>(items) * ka.nsplit * 128 * 512;
     }
-    cudaError_t e = a.c_scale ? launch<true>(ka, items, st) : launch<false>(ka, items, st);
-    if (e == cudaSuccess && ka.nsplit > 1) {
+    const sa_status s = a.c_scale ? launch<true>(ka, items, st) : launch<false>(ka, items, st);
+    if (s == SA_OK && ka.nsplit > 1) {
         const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
         constexpr int kPer = kCombThreads / 32;
-        e = launch_pdl(mla_latent_combine_kernel, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)), dim3(kCombThreads), 0,
-                       st, ka);
+        return launch_status(launch_pdl(mla_latent_combine_kernel, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),
+                                        dim3(kCombThreads), 0, st, ka));
     }
-    return launch_status(e);
+    return s;
 }
 
 }  // namespace sa

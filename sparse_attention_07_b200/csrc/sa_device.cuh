@@ -107,6 +107,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// Arrive on a barrier of another CTA of the cluster, ordering this thread's
+// earlier writes only within its own CTA: for reports about the CTA's own shared
+// memory to the thread that issues its tensor-core work.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("fence.acq_rel.cta;\n\tmbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+                 : "memory");
+}
+
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* b, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -226,6 +234,17 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t
         : "memory");
 }
 
+// Four rows of a 2D tensor (box one row high) at column x, landing one after the
+// other; a row outside the tensor reads as zeros.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, uint32_t bar, int x, int r0, int r1, int r2,
+                                            int r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
+        "%5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
+}
+
 // Contiguous global -> shared bulk copy into this CTA's shared memory,
 // completing `bytes` transactions on `bar`.  Both addresses 16-byte aligned,
 // bytes a multiple of 16.
@@ -256,11 +275,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// As fence_proxy_async_smem, for writes to the shared memory of any CTA of the cluster.
-__device__ __forceinline__ void fence_proxy_async_cluster() {
-    asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
 }
 
 // Order this thread's generic-proxy shared-memory writes before later
@@ -371,6 +385,15 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
+}
+// True in one lane of a converged warp.  MMAs issued under it from a
+// warp-uniform loop keep their descriptors in uniform registers: a run of
+// M = 128, N = 64 pair products issues every 25 cycles, against 48 from code
+// that only one lane reaches.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 // Arrive once on `bar` of both CTAs when every pair op this thread issued so far is done.
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
@@ -537,6 +560,16 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, uint32_t scale2) {
     const uint32_t l = ((lo >> 4) & 0x07F007F0u) | (lo & 0x80008000u);
     const uint32_t h = ((hi >> 4) & 0x07F007F0u) | (hi & 0x80008000u);
     return make_uint2(hmul2_bf16(hmul2_bf16(l, k2p120), scale2), hmul2_bf16(hmul2_bf16(h, k2p120), scale2));
+}
+
+
+// The same four values in the order 0, 2, 1, 3, which takes fewer shifts: codes
+// 1 and 3 already stand in the upper bytes of the two halves.
+__device__ __forceinline__ uint2 e4m3x4_to_bf16x4_0213(uint32_t w, uint32_t scale2) {
+    constexpr uint32_t k2p120 = 0x7B807B80u;
+    const uint32_t e = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
+    const uint32_t o = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
+    return make_uint2(hmul2_bf16(hmul2_bf16(e, k2p120), scale2), hmul2_bf16(hmul2_bf16(o, k2p120), scale2));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
