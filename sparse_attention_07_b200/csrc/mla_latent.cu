@@ -13,20 +13,19 @@
 //    their scores and softmax state, so nothing is exchanged between the two
 //    but the cache rows themselves.
 //  * Keys go by in tiles of 64.  A CTA supplies 32 rows of each as its half of the
-//    score product's B operand (576 dims, K-major) and 256 dims of all 64 as its
-//    half of the aggregation's (MN-major).  One warp resolves pool rows and issues
-//    the TMA loads.  bf16 rows (of a prefix: whole pages) land in the operands.
-//    e4m3 rows are gathered four at a time into a two-slot ring; eight warps turn
-//    them into bf16 in registers, exactly, and store them to one-stage operands,
-//    four warps each: the score operand is refilled while the aggregation runs and
-//    the other way round.  Latent dims stand there in the order 0, 2, 1, 3 of each
-//    four (fewer shifts), in the query and the output columns alike.
-//    Measured and dropped: plain loads to registers (the shared memory taken
-//    leaves the L1 too little room for a tile in flight), cp.async (its requests
-//    hold up the barrier arrivals between the CTAs: 2000 cycles per tile), and
-//    sending the rows that the partner aggregates through distributed shared
-//    memory (16 KB per tile at 20 bytes per clock from stores, 10 from bulk copies
-//    and st.async, and a cluster-scope release per tile).
+//    score product's B operand (576 dims, K-major, two stages) and 256 dims of all
+//    64 as its half of the aggregation's (MN-major).  bf16 rows (of a prefix: whole
+//    pages) are TMA-loaded into the operands.  e4m3 rows are loaded to registers by
+//    eight warps, a tile ahead, turned into bf16 there, exactly, and stored to the
+//    operands, four warps each; one warp resolves their pool rows and scales, one
+//    gathers the RoPE rows by TMA.  Latent dims stand in the order 0, 2, 1, 3 of
+//    each four (fewer shifts), in the query and the output columns alike.
+//    Measured and dropped for the e4m3 rows: cp.async into shared memory (its
+//    requests hold up the barrier arrivals between the CTAs: 2000 cycles per
+//    tile), four-row TMA gathers (200 cycles each beside the products, 16 per
+//    tile), and sending the rows that the partner aggregates through distributed
+//    shared memory (16 KB per tile at 20 bytes per clock from stores, 10 from bulk
+//    copies and st.async, and a cluster-scope release per tile).
 //  * Four softmax warps: thread = (row, half of the tile's keys).  Online base-2
 //    softmax; the two threads of a row exchange tile maxima through shared
 //    memory, O is rescaled only when a maximum grows by more than 2^8.  P goes
@@ -54,31 +53,30 @@ constexpr int kVStage = 4 * kVSlice;
 constexpr int kSmxWarps = 4, kLoadWarps = 4;  // loading warps of either operand
 constexpr int kKWarp0 = kSmxWarps, kVWarp0 = kKWarp0 + kLoadWarps;
 constexpr int kMmaWarp = kVWarp0 + kLoadWarps;
-constexpr int kTmaWarp = kMmaWarp + 1, kTmaWarps = 3;
-constexpr int kThreads = 32 * (kTmaWarp + kTmaWarps);
+constexpr int kTmaWarp = kMmaWarp + 1;      // e4m3: RoPE rows, score operand reported; bf16: every load
+constexpr int kRowWarp = kTmaWarp + 1;      // e4m3: rows resolved
+constexpr int kVReportWarp = kRowWarp + 1;  // e4m3: aggregation operand reported
+constexpr int kThreads = 32 * (kVReportWarp + 1);
 constexpr int kORow = 512 * 4 + 16;  // a staged output row (padded)
-
-// A raw slot (e4m3): this CTA's 32 latent rows of a tile, the partner's, and the
-// scale words of the tile's 64 rows.
-constexpr int kRawOther = kOwn * 512, kRawScale = 2 * kRawOther, kRawSlot = kRawScale + kNK * 4;
 
 template <bool kQ8>
 struct Smem {
-    static constexpr int kStages = kQ8 ? 1 : 2;  // of the latent slices of K, and of V; RoPE slice: two
+    static constexpr int kRope = kQ8 ? 3 : 2;    // of the RoPE slice
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 9 * kQSlice;
-    static constexpr int kOffR = kOffK + kStages * 8 * kKSlice;
-    static constexpr int kOffV = kOffR + 2 * kKSlice;
-    static constexpr int kOffP = kOffV + kStages * kVStage;
-    static constexpr int kOffRaw = kOffP + kRows * 128;
-    static constexpr int kEnd = kOffRaw + (kQ8 ? 2 * kRawSlot : 0);
+    static constexpr int kOffR = kOffK + 2 * 8 * kKSlice;
+    static constexpr int kOffV = kOffR + kRope * kKSlice;
+    static constexpr int kOffP = kOffV + 2 * kVStage;
+    static constexpr int kEnd = kOffP + kRows * 128;
     static constexpr int kBytes = kEnd + 1024;
     static_assert(kOffK % 1024 == 0 && kOffR % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms are 1024-byte aligned");
-    static_assert(kRawSlot % 128 == 0, "TMA destinations are 128-byte aligned");
-    static_assert(kBytes <= 232448 - 3072, "shared memory budget");
+    static_assert(kBytes <= 232448 - 4096, "shared memory budget");
     static_assert(kRows * kORow <= kEnd, "the output rows fit");
 };
 
+// Tiles whose rows are resolved ahead: the warps of the score operand run up to three
+// tiles ahead of the aggregation's.
+constexpr int kRing = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 0;    // two 256-dim products, 128 columns each
 constexpr uint32_t kColS = 256;  // two score buffers of 32 columns
@@ -100,29 +98,39 @@ struct Args {
     float* ws_ml;  // [item][nsplit][128][2]: m, l
 };
 
-// warp_wait that polls without suspending.
-__device__ __forceinline__ bool warp_spin(uint64_t* b, uint32_t parity, const WaitCtx& w, int site) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) {
-        unsigned long long t0 = 0;
-        for (uint32_t n = 0; !mbar_test_wait(b, parity); ++n) {
-            if ((n & 63u) != 63u) continue;
-            if (*w.abort) {
-                ok = 0;
-                break;
-            }
-            const unsigned long long now = global_ns();
-            if (t0 == 0) t0 = now;
-            if (now - t0 > w.limit_ns) {
-                record_error(w.err, site);
-                *w.abort = 1;
-                ok = 0;
-                break;
+// Waits of this kernel.  The code is small (some thirty of them are inlined, and
+// the roles' loops together have to stay in the instruction cache): a wait that
+// runs out leaves its site in the CTA's abort word, and the CTA's end records it.
+struct Waits {
+    volatile int* abort;
+    uint32_t limit_ns;
+
+    __device__ __forceinline__ static uint32_t now() {
+        uint32_t t;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+        return t;
+    }
+    // (one lane)
+    __device__ __forceinline__ bool one(uint64_t* b, uint32_t parity, int site) const {
+        if (mbar_try_wait(b, parity)) return true;
+        const uint32_t t0 = now();
+#pragma unroll 1
+        while (!mbar_try_wait(b, parity)) {
+            if (*abort) return false;
+            if (now() - t0 > limit_ns) {
+                *abort = site;
+                return false;
             }
         }
+        return true;
     }
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
-}
+    // The whole warp leaves together.
+    __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity, int site) const {
+        int ok = 1;
+        if ((threadIdx.x & 31) == 0) ok = one(b, parity, site) ? 1 : 0;
+        return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    }
+};
 
 // What one item covers.
 struct Item {
@@ -154,13 +162,10 @@ __device__ __forceinline__ int key_page(const LatentArgs& a, const Item& it, int
     const int64_t at = static_cast<int64_t>(it.seq) * a.pages_per_seq + pos / kPage;
     return a.page_table ? a.page_table[at] : (at < a.pool_pages ? static_cast<int>(at) : -1);
 }
-__device__ __forceinline__ int key_row(const LatentArgs& a, int pos, int page) {
-    if (pos < 0) return -1;
-    if (page < 0 || page >= a.pool_pages) {
-        record_error(a.err, kErrMlaIndex);
-        return 0;
-    }
-    return page * kPage + (pos % kPage);
+__device__ __forceinline__ int key_row(const LatentArgs& a, int pos, int page, bool& broken) {
+    const bool ok = page >= 0 && page < a.pool_pages;
+    if (pos >= 0 && !ok) broken = true;
+    return pos < 0 ? -1 : ok ? page * kPage + (pos % kPage) : 0;
 }
 
 // Pool rows and scale words of 32 keys (lane = key) of the tiles to come: the next
@@ -169,6 +174,7 @@ template <bool kQ8>
 struct Rows {
     int row, next, pos2, page2, pos3;
     uint32_t sc, sc_next;
+    bool broken;
 
     __device__ __forceinline__ uint32_t scale_word(const LatentArgs& a, int r) const {
         return kQ8 && r >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(a.c_scale + r * a.s_ld)) : 0x7F7F7F7Fu;
@@ -180,8 +186,9 @@ struct Rows {
         pos3 = key_position(a, it, 3 < nt, slot + 3 * kNK);
         const int g0 = key_page(a, it, p0), g1 = key_page(a, it, p1);
         page2 = key_page(a, it, pos2);
-        row = key_row(a, p0, g0);
-        next = key_row(a, p1, g1);
+        broken = false;
+        row = key_row(a, p0, g0, broken);
+        next = key_row(a, p1, g1, broken);
         sc = scale_word(a, row);
         sc_next = scale_word(a, next);
     }
@@ -189,7 +196,7 @@ struct Rows {
     __device__ __forceinline__ void advance(const LatentArgs& a, const Item& it, int nt, int slot, int t) {
         row = next;
         sc = sc_next;
-        next = key_row(a, pos2, page2);
+        next = key_row(a, pos2, page2, broken);
         sc_next = scale_word(a, next);
         pos2 = pos3;
         page2 = key_page(a, it, pos2);
@@ -218,12 +225,12 @@ __device__ __forceinline__ void st_smem_v4(uint32_t addr, uint4 v) {
                  : "memory");
 }
 
-__device__ __forceinline__ void st_smem_u32(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_smem_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+// Volatile: issued a tile ahead of its use, where it stands, and not sunk to it.
+__device__ __forceinline__ uint4 ld_row16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
     return v;
 }
 __device__ __forceinline__ uint4 ld_smem_v4(uint32_t addr) {
@@ -233,12 +240,39 @@ __device__ __forceinline__ uint4 ld_smem_v4(uint32_t addr) {
 }
 
 // Sixteen e4m3 dims -> two 16-byte bf16 pieces, each four in the order 0, 2, 1, 3.
-__device__ __forceinline__ void convert16(uint4 u, uint32_t scale, uint4& lo, uint4& hi) {
-    const uint32_t f = q8_scale_bf16x2(scale);
+__device__ __forceinline__ void convert16(uint4 u, uint32_t f, uint4& lo, uint4& hi) {
     const uint2 v0 = e4m3x4_to_bf16x4_0213(u.x, f), v1 = e4m3x4_to_bf16x4_0213(u.y, f);
     const uint2 v2 = e4m3x4_to_bf16x4_0213(u.z, f), v3 = e4m3x4_to_bf16x4_0213(u.w, f);
     lo = make_uint4(v0.x, v0.y, v1.x, v1.y);
     hi = make_uint4(v2.x, v2.y, v3.x, v3.y);
+}
+__device__ __forceinline__ void times4(uint4& v, uint32_t f) {
+    v = make_uint4(hmul2_bf16(v.x, f), hmul2_bf16(v.y, f), hmul2_bf16(v.z, f), hmul2_bf16(v.w, f));
+}
+
+// Gather 32 rows (lane = row) of `bytes` each to dst on.  Issued by one lane of the
+// converged warp: from divergent lanes a gather takes longer than its 80 cycles.
+__device__ __forceinline__ void gather32(const void* map, uint32_t dst, int bytes, uint32_t bar, int row) {
+#pragma unroll 1
+    for (int g = 0; g < 8; ++g) {
+        int r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(0xffffffffu, row, 4 * g + i);
+        if (elect_one()) tma_gather4(dst + 4 * g * bytes, map, bar, 0, r[0], r[1], r[2], r[3]);
+        __syncwarp();
+    }
+}
+
+// The loads of the last of `issued` tiles, one per stage, have landed (fixed limit).
+__device__ __forceinline__ void drain(int* abort_word, uint64_t* bars, int stages, int issued, int lane) {
+    if (lane == 0) {
+        int none = 0;
+        const Waits w{&none, static_cast<uint32_t>(kWaitLimitNs)};
+#pragma unroll 1
+        for (int t = max(0, issued - stages); t < issued; ++t)
+            if (!w.one(&bars[t % stages], static_cast<uint32_t>(t / stages & 1), 14)) *abort_word = 14;
+    }
+    __syncwarp();
 }
 
 __device__ __forceinline__ bool bad4(uint4 v) {
@@ -249,12 +283,14 @@ template <bool kQ8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_latent_kernel(const Args ka, const __grid_constant__ Maps maps) {
     pdl_trigger();
     using S = Smem<kQ8>;
-    constexpr int kStages = S::kStages;
     const LatentArgs& a = ka.a;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t bar_raw[2], bar_rawfree[2];  // e4m3: the ring
-    __shared__ uint64_t bar_kst[2], bar_vst[2];      // loads straight into an operand have landed (e4m3: RoPE slice)
+    __shared__ uint64_t bar_rows[kRing], bar_rowsfree[kRing];  // e4m3: rows and scale words of a tile's keys
+    __shared__ int s_row[kRing][kNK];
+    __shared__ uint32_t s_scale[kRing][kNK];
+    __shared__ uint64_t bar_kst[3], bar_vst[2];      // loads straight into an operand have landed (e4m3: RoPE slice)
+    __shared__ uint64_t bar_kdone[2], bar_vdone[2];        // e4m3: the loading warps have stored an operand
     // a stage is visible to the tensor cores, the scores are read, P is written: waited for by the
     // issuing thread (the even CTA's copies are used)
     __shared__ uint64_t bar_kfull[2], bar_vfull[2], bar_sfree[2], bar_pfull;
@@ -276,21 +312,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     const int tiles = (it.n_keys + kNK - 1) / kNK;
     const int t0 = static_cast<int>(static_cast<int64_t>(split) * tiles / ka.nsplit);
     const int nt = static_cast<int>(static_cast<int64_t>(split + 1) * tiles / ka.nsplit) - t0;
-    WaitCtx wc{a.err, &s_abort};
+    const Waits wait{&s_abort, wait_limit_of(a.err)};
 
     if (tid == 0) {
         s_abort = 0;
         s_fail[0] = s_fail[1] = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar_raw[i], 2);
-            mbar_init(&bar_rawfree[i], 2 * kLoadWarps);
-            mbar_init(&bar_kst[i], 1);
+            mbar_init(&bar_kdone[i], kLoadWarps);
+            mbar_init(&bar_vdone[i], kLoadWarps);
             mbar_init(&bar_vst[i], 1);
-            mbar_init(&bar_kfull[i], kQ8 ? 2 * kLoadWarps : 2);
-            mbar_init(&bar_vfull[i], kQ8 ? 2 * kLoadWarps : 2);
+            mbar_init(&bar_kfull[i], 2);
+            mbar_init(&bar_vfull[i], 2);
             mbar_init(&bar_sfree[i], 2 * kSmxWarps);
             mbar_init(&bar_s[i], 1);
             mbar_init(&bar_o[i], 1);
+        }
+        for (int i = 0; i < 3; ++i) mbar_init(&bar_kst[i], 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&bar_rows[i], 2);
+            mbar_init(&bar_rowsfree[i], 2 * kLoadWarps + 1);
         }
         mbar_init(&bar_pfull, 2 * kSmxWarps);
         mbar_init(&bar_final, 1);
@@ -301,47 +341,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         tmem_relinquish_pair();
     }
 
-    const uint32_t kbase = smem_u32(sm + S::kOffK), vbase = smem_u32(sm + S::kOffV), raw = smem_u32(sm + S::kOffRaw);
+    const uint32_t kbase = smem_u32(sm + S::kOffK), vbase = smem_u32(sm + S::kOffV);
     const int own0 = static_cast<int>(rank) * kOwn, other0 = kOwn - own0;  // this CTA's keys of a tile, the partner's
-    // TMA warps.  e4m3: one for the latent rows of this CTA's keys of a tile, one for the partner's, one
-    // for the RoPE rows (a warp issues a four-row gather every 80 cycles, whatever the rows' size).
-    // bf16: the first loads whole tiles.
-    const int tw = warp - kTmaWarp;
-    const int key0 = kQ8 ? (tw == 1 ? other0 : own0) : 0;
-    Rows<kQ8> keys;
+    // keys of a tile whose rows a warp resolves: e4m3: this CTA's half and the partner's; bf16: the first
+    Rows<kQ8> keys, others;
     if (warp >= kTmaWarp) {
-        if (lane == 0) {
-            tma_prefetch_desc(&maps.c);
+        if (warp == kTmaWarp && lane == 0) {
+            if (!kQ8) tma_prefetch_desc(&maps.c);
             if (!kQ8) tma_prefetch_desc(&maps.cv);
             tma_prefetch_desc(&maps.kr);
         }
-        if (kQ8 || tw == 0) keys.start(a, it, nt, t0 * kNK + key0 + lane);
-    } else {
+        if (warp == (kQ8 ? kRowWarp : kTmaWarp)) keys.start(a, it, nt, t0 * kNK + (kQ8 ? own0 : 0) + lane);
+        if (kQ8 && warp == kRowWarp) others.start(a, it, nt, t0 * kNK + other0 + lane);
+    } else if (warp < kTmaWarp) {
         // the query rows, as the K-major A operand: row r of this CTA, 16-byte piece c of its 72
         // (512 latent dims, then 64 RoPE dims); rows that are not live are zero
         const uint32_t sQ = smem_u32(sm + S::kOffQ);
         const int rows = it.tokens * a.H - static_cast<int>(rank) * kRows;
         const int64_t q0 = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + rank * kRows;
-        constexpr int kQThreads = 32 * kTmaWarp, kFlight = 6;
+        // a negative scale is moved to the queries: the softmax takes maxima of unscaled scores
+        const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+        // a warp per row, two rows in flight: pieces lane, lane + 32, and in eight lanes lane + 64
 #pragma unroll 1
-        for (int i0 = tid; i0 < kRows * 72; i0 += kFlight * kQThreads) {
-            uint4 v[kFlight];
+        for (int r0 = warp; r0 < kRows; r0 += 2 * kTmaWarp) {
+            uint4 x[2][3];
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-                const int i = i0 + k * kQThreads, r = i / 72, c = i % 72;
-                const bool in = i < kRows * 72 && r < rows;
-                const uint4* src = c < 64 ? static_cast<const uint4*>(a.q_lat) + (q0 + r) * 64 + c
-                                          : static_cast<const uint4*>(a.q_rope) + (q0 + r) * 8 + (c - 64);
-                v[k] = make_uint4(0u, 0u, 0u, 0u);
-                if (in) v[k] = __ldg(src);
+            for (int k = 0; k < 2; ++k) {
+                const int r = r0 + k * kTmaWarp;
+                const uint4* lat = static_cast<const uint4*>(a.q_lat) + (q0 + r) * 64 + lane;
+                const uint4* rope = static_cast<const uint4*>(a.q_rope) + (q0 + r) * 8 + lane;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    x[k][j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < rows && (j < 2 || lane < 8)) x[k][j] = __ldg(j < 2 ? lat + 32 * j : rope);
+                }
             }
 #pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-                const int i = i0 + k * kQThreads, r = i / 72, c = i % 72;
-                if (kQ8 && c < 64)
-                    v[k] = make_uint4(__byte_perm(v[k].x, v[k].y, 0x5410), __byte_perm(v[k].x, v[k].y, 0x7632),
-                                      __byte_perm(v[k].z, v[k].w, 0x5410), __byte_perm(v[k].z, v[k].w, 0x7632));
-                if (i < kRows * 72) st_smem_v4(sQ + (c >> 3) * kQSlice + r * 128 + (((c & 7) ^ (r & 7)) << 4), v[k]);
+            for (int k = 0; k < 2; ++k) {
+                const int r = r0 + k * kTmaWarp;
+                if (r >= kRows) break;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    uint4 v = x[k][j];
+                    v = make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
+                    if (kQ8 && j < 2)
+                        v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                                       __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+                    if (j < 2 || lane < 8)
+                        st_smem_v4(sQ + ((lane >> 3) + 4 * j) * kQSlice + r * 128 + (((lane & 7) ^ (r & 7)) << 4), v);
+                }
             }
         }
         fence_proxy_async_smem();
@@ -354,38 +402,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 
     if (nt <= 0) {
         // no keys: fall through (the softmax warps write the empty result)
-    } else if (warp >= kTmaWarp) {
-        // ------------------------------------------ loads
-        int issued = 0, issued_v = 0;
-        if (kQ8) {
-            for (int t = 0; t < nt; ++t) {
-                const int st = t & 1;
-                // the slot has been read; the RoPE slice's products are done
-                if (t >= 2 && !warp_wait(tw == 2 ? &bar_s[st] : &bar_rawfree[st], static_cast<uint32_t>((t >> 1) & 1) ^ 1, wc,
-                                         kErrLatWait | 1))
-                    break;
-                uint64_t* landed = tw == 2 ? &bar_kst[st] : &bar_raw[st];
-                const uint32_t bar = smem_u32(landed);
-                const uint32_t dst = tw == 2 ? smem_u32(sm + S::kOffR) + st * kKSlice : raw + st * kRawSlot + tw * kRawOther;
-                const int bytes = tw == 2 ? 128 : 512;  // per row
-                const CUtensorMap* map = tw == 2 ? &maps.kr : &maps.c;
-                if (tw < 2) st_smem_u32(raw + st * kRawSlot + kRawScale + 4 * (key0 + lane), keys.sc);
-                __syncwarp();
-                if (elect_one()) mbar_arrive_expect_tx(landed, kOwn * bytes);
-                __syncwarp();
-                // (under elect_one: from divergent lanes the issue is slower)
-#pragma unroll
-                for (int g = 0; g < 8; ++g) {
-                    int r[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(0xffffffffu, keys.row, 4 * g + i);
-                    if (elect_one()) tma_gather4(dst + 4 * g * bytes, map, bar, 0, r[0], r[1], r[2], r[3]);
-                    __syncwarp();
-                }
-                issued = t + 1;
-                keys.advance(a, it, nt, t0 * kNK + key0 + lane, t + 1);
+    } else if (kQ8 && warp == kTmaWarp) {
+        // ------------------------------------------ e4m3: RoPE slice loaded, score operand reported
+        // (a fence in a loading thread would wait for its stores and loads; the operand's bytes are in this
+        // CTA, so the report to the issuing thread orders no more than that)
+        const uint32_t full = mapa_u32(smem_u32(&bar_kfull[0]), 0);
+        int issued = 0;
+#pragma unroll 1
+        for (int t = -2; t < nt; ++t) {
+            if (t >= 0) {
+                if (!wait(&bar_kdone[t & 1], static_cast<uint32_t>(t >> 1 & 1), 1)) break;
+                fence_proxy_async_smem();
+                if (!wait(&bar_kst[t % 3], static_cast<uint32_t>(t / 3 & 1), 2)) break;
+                if (lane == 0) mbar_arrive_remote(full + 8 * (t & 1));
             }
-        } else if (tw == 0) {
+            // RoPE slice of tile n (three of them: free once the scores of tile n - 3 are there, so that the
+            // gather never stands between an operand and its report)
+            const int n = t + 2, f = n - 3, st = n % kRing;
+            if (n < nt) {
+                if (f >= 0 && !wait(&bar_s[f & 1], static_cast<uint32_t>(f >> 1 & 1), 3)) break;
+                if (!wait(&bar_rows[st], static_cast<uint32_t>(n / kRing & 1), 4)) break;
+                const int row = s_row[st][own0 + lane];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
+                if (elect_one()) mbar_arrive_expect_tx(&bar_kst[n % 3], kKSlice);
+                gather32(&maps.kr, smem_u32(sm + S::kOffR) + n % 3 * kKSlice, 128, smem_u32(&bar_kst[n % 3]), row);
+                issued = n + 1;
+            }
+        }
+        drain(&s_abort, bar_kst, 3, issued, lane);
+    } else if (kQ8 && warp == kRowWarp) {
+        // ------------------------------------------ e4m3: pool rows and scales, as far ahead as the ring goes
+#pragma unroll 1
+        for (int h = 0; h < 2 * nt; ++h) {  // half tiles: the lanes' own keys, then the partner's
+            const int t = h >> 1, st = t % kRing, key0 = h & 1 ? other0 : own0;
+            if (t >= kRing && !wait(&bar_rowsfree[st], static_cast<uint32_t>(t / kRing & 1) ^ 1, 5)) break;
+            s_row[st][key0 + lane] = keys.row;
+            s_scale[st][key0 + lane] = keys.sc;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_rows[st]);
+            keys.advance(a, it, nt, t0 * kNK + key0 + lane, t + 1);
+            const Rows<kQ8> x = keys;  // (one copy of the code for both)
+            keys = others;
+            others = x;
+        }
+        if (keys.broken || others.broken) record_error(a.err, kErrMlaIndex);
+        __syncwarp();
+    } else if (kQ8 && warp == kVReportWarp) {
+        // ------------------------------------------ e4m3: aggregation operand reported
+        const uint32_t full = mapa_u32(smem_u32(&bar_vfull[0]), 0);
+#pragma unroll 1
+        for (int t = 0; t < nt; ++t) {
+            if (!wait(&bar_vdone[t & 1], static_cast<uint32_t>(t >> 1 & 1), 6)) break;
+            fence_proxy_async_smem();
+            if (lane == 0) mbar_arrive_remote(full + 8 * (t & 1));
+        }
+        __syncwarp();
+    } else if (!kQ8 && warp == kTmaWarp) {
+        // ------------------------------------------ bf16: loads
+        int issued = 0, issued_v = 0;
+        {
             // A tile is one page: the row of the tile's key 0 (keys past the last one are masked, and
             // cleaned in the aggregation operand).  The score operand of a tile comes before the
             // aggregation operand of the tile before it, as their stages become free.
@@ -395,7 +471,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 const int row1 = row0, st = t & 1;
                 if (t < nt) {
                     row0 = __shfl_sync(0xffffffffu, keys.row, 0);
-                    if (t >= 2 && !warp_wait(&bar_s[st], par, wc, kErrLatWait | 1)) break;
+                    if (t >= 2 && !wait(&bar_s[st], par, 1)) break;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&bar_kst[st], 9 * kKSlice);
                         for (int sl = 0; sl < 8; ++sl)
@@ -408,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 }
                 if (t >= 1) {
                     const int u = t - 1, vs = u & 1;
-                    if (u >= 2 && !warp_wait(&bar_o[vs], static_cast<uint32_t>((u >> 1) & 1) ^ 1, wc, kErrLatWait | 2)) break;
+                    if (u >= 2 && !wait(&bar_o[vs], static_cast<uint32_t>((u >> 1) & 1) ^ 1, 2)) break;
                     if (elect_one()) {
                         mbar_arrive_expect_tx(&bar_vst[vs], kVStage);
                         for (int sl = 0; sl < 4; ++sl)
@@ -419,82 +495,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     issued_v = t;
                 }
             }
+            if (keys.broken) record_error(a.err, kErrMlaIndex);
+            drain(&s_abort, bar_kst, 2, issued, lane);
+            drain(&s_abort, bar_vst, 2, issued_v, lane);
         }
-        // every load has landed (fixed limit) before the CTA can exit
-        if (lane == 0) {
-            int dummy = 0;
-            WaitCtx dw(a.err, reinterpret_cast<volatile int*>(&dummy), kWaitLimitNs);
-            for (int t = max(0, issued - 2); t < issued; ++t)
-                mbar_wait(kQ8 && tw < 2 ? &bar_raw[t & 1] : &bar_kst[t & 1], static_cast<uint32_t>(t >> 1 & 1), dw, kErrLatWait | 14);
-            for (int t = max(0, issued_v - 2); t < issued_v; ++t)
-                mbar_wait(&bar_vst[t & 1], static_cast<uint32_t>(t >> 1 & 1), dw, kErrLatWait | 15);
-        }
-        __syncwarp();
     } else if (kQ8 && warp >= kKWarp0 && warp < kMmaWarp) {
-        // ------------------------------------------ e4m3 rows into an operand.  Unit i of a warp: 16 dims
-        // per lane of row i (scores: own row 8 lw + i) or of rows i and 8 + i (aggregation: rows 16 lw + ..
-        // of the tile, lanes 16 .. 31 the second).  One code for both: they differ in what a lane's
-        // pieces start from.
+        // ------------------------------------------ e4m3 rows into an operand.  Scores: own rows 8 lw ..
+        // 8 lw + 7 of a tile, 32 pieces of 16 dims each; aggregation: rows 16 lw .. 16 lw + 7 of it in the
+        // lower half warp, 16 lw + 8 .. in the upper, the 16 pieces of this CTA's 256 dims each.  Unit i of a
+        // lane: of row 2 (i / 2) + odd, odd = lane / 4 % 2, piece 8 (lane / 8) + lane % 4 (+ 4 where i + odd
+        // is odd): the eight lanes of a load or store phase touch distinct banks, lanes 0 .. 3 in an even
+        // row, lanes 4 .. 7 in the odd one next to it (its swizzle differs in the lowest bit).
         const bool v = warp >= kVWarp0;
-        const int lw = warp - (v ? kVWarp0 : kKWarp0);
-        const int vrow = 16 * lw + 8 * (lane >> 4);             // aggregation: the lane's row of unit 0
-        const bool from_own = !v || (vrow & kOwn) == own0;      // (warp-uniform)
-        const int q = v ? vrow & (kOwn - 1) : 8 * lw;           // its index among those 32 rows
-        const int blk = lane >> 3 & 1;
-        // where the lane's 16 bytes of unit 0 stand in the slot
-        const uint32_t src0 = raw + (from_own ? 0 : kRawOther) + q * 512 +
-                              (v ? 256 * blk + 128 * rank + 16 * (lane & 7) : 16 * lane);
-        const uint32_t sc0 = raw + kRawScale + 4 * (v ? vrow + (lane & 7) : own0 + 8 * lw + (lane & 7));  // scale word of unit lane % 8
-        const int sc_shift = v ? 16 * blk + 8 * static_cast<int>(rank) : lane & 24;
-        // pieces c, c ^ 1 of slice lane / 4; odd slices store theirs in the other order, so that the
-        // eight lanes of a store phase touch distinct banks
-        const bool odd = lane >> 2 & 1;
-        const uint32_t c = 2 * (lane & 3) + (odd ? 1 : 0);
-        const uint32_t dst0 = v ? vbase + (lane >> 2 & 3) * kVSlice + vrow * 128 : kbase + (lane >> 2) * kKSlice + 8 * lw * 128;
+        const int lw = warp - (v ? kVWarp0 : kKWarp0), odd = lane >> 2 & 1;
+        const int row0 = v ? 16 * lw + 8 * (lane >> 4) : own0 + 8 * lw;    // of the tile
+        const int blk = v ? lane >> 3 & 1 : lane >> 3;                     // 128-dim block of the lane's pieces
+        // unit 0's bytes of row 0, had the lane an even row
+        const uint8_t* src0 = static_cast<const uint8_t*>(a.c_cache) + (v ? 256 * blk + 128 * rank : 128 * blk) + 16 * (lane & 3);
+        const int sc_shift = v ? 16 * blk + 8 * static_cast<int>(rank) : 8 * blk;
+        const uint32_t slice0 = v ? vbase + 2 * blk * kVSlice + row0 * 128 : kbase + 2 * blk * kKSlice + 8 * lw * 128;
+        const uint32_t slice = v ? kVSlice : kKSlice;                      // the next 64 dims
         uint64_t* freed = v ? bar_o : bar_s;
-        const uint32_t full = mapa_u32(smem_u32(v ? &bar_vfull[0] : &bar_kfull[0]), 0);
-        uint4 u[8];
-        uint32_t sc = 0;
-        auto fetch = [&](int t) {
-            if (!warp_wait(&bar_raw[t & 1], static_cast<uint32_t>(t >> 1 & 1), wc, kErrLatWait | 13)) return false;
-            const uint32_t slot = (t & 1) * kRawSlot;
+        // Two steps per tile, four units each (row 4 step + 2 k + odd, pieces as above); two steps' loads
+        // are under way.  Rolled up like this the loop is small enough to stay in the instruction cache
+        // beside the other roles' (a body of eight units ran at the pace of instruction fetches).
+        struct Step {
+            uint4 u[4];
+            uint32_t sc;  // scale word of row lane % 8
+        };
+        auto fetch = [&](int q, Step& x) {
+            if (q >= 2 * nt) return true;
+            const int t = q >> 1, st = t % kRing;
+            if ((q & 1) == 0 && !wait(&bar_rows[st], static_cast<uint32_t>(t / kRing & 1), 7)) return false;
+            int row[2];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = ld_smem_v4(src0 + slot + i * 512);
-            sc = ld_smem_u32(sc0 + slot);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_rawfree[t & 1]);
+            for (int k = 0; k < 2; ++k) row[k] = s_row[st][row0 + 4 * (q & 1) + 2 * k + odd];
+            x.sc = s_scale[st][row0 + (lane & 7)];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint8_t* src = src0 + row[k] * a.c_ld;
+                x.u[2 * k] = x.u[2 * k + 1] = make_uint4(0u, 0u, 0u, 0u);
+                if (row[k] >= 0) {
+                    x.u[2 * k] = ld_row16(src + 64 * odd);
+                    x.u[2 * k + 1] = ld_row16(src + 64 * (odd ^ 1));
+                }
+            }
+            if (q & 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
+            }
             return true;
         };
-        bool ok = fetch(0);
-        for (int t = 0; ok && t < nt; ++t) {
-            uint4 w[8][2];
+        Step cur, next;
+        bool ok = fetch(0, cur) && fetch(1, next);
+#pragma unroll 1
+        for (int q = 0; ok && q < 2 * nt; ++q) {
+            const int t = q >> 1, r0 = 4 * (q & 1) + odd;
+            // a drafted row's non-finite block (byte 255) stays out of the aggregation: its finite codes times 0
+            const int drafted_from = v && a.tree ? it.past - (t0 + t) * kNK - row0 : kNK;
+            uint4 w[4][2];
+            uint32_t big = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint4 lo, hi;
-                convert16(u[i], __shfl_sync(0xffffffffu, sc, (lane & 16) + i) >> sc_shift & 255u, lo, hi);
-                w[i][0] = odd ? hi : lo;
-                w[i][1] = odd ? lo : hi;
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t e = __shfl_sync(0xffffffffu, cur.sc, (lane & 16) + r0 + (i & 2)) >> sc_shift & 255u;
+                const bool hide = e == 255u && r0 + (i & 2) >= drafted_from;
+                convert16(cur.u[i], hide ? 0u : q8_factor_bf16x2(e), w[i][0], w[i][1]);
+                big |= e;
             }
-            // the next tile's codes, before the wait for the operand: the slot is free that much earlier
-            if (t + 1 < nt && !fetch(t + 1)) break;
-            const int tile0 = (t0 + t) * kNK;
-            if (v && a.tree && tile0 + kNK > it.past) {  // drafted rows: non-finite contents stay out of the aggregation
+            if (__any_sync(0xffffffffu, big > 127u)) {  // scales of 2 and above: some may need a second factor
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (tile0 + vrow + i >= it.past && (bad4(w[i][0]) || bad4(w[i][1]))) w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t f = q8_excess_bf16x2(__shfl_sync(0xffffffffu, cur.sc, (lane & 16) + r0 + (i & 2)) >> sc_shift & 255u);
+                    times4(w[i][0], f);
+                    times4(w[i][1], f);
+                }
             }
-            if (t >= 1 && !warp_wait(&freed[(t - 1) & 1], static_cast<uint32_t>(t - 1 >> 1 & 1), wc, kErrLatWait | 2)) break;
+            cur = next;
+            if (!fetch(q + 2, next)) break;
+            const int tf = t - 2;  // the tile whose products free the stage
+            if ((q & 1) == 0 && tf >= 0 && !wait(&freed[tf & 1], static_cast<uint32_t>(tf >> 1 & 1), 8)) break;
+            const uint32_t stage = slice0 + (t & 1) * (v ? kVStage : 8 * kKSlice);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t off = i * 128 + ((c ^ i) << 4);
-                st_smem_v4(dst0 + off, w[i][0]);
-                st_smem_v4(dst0 + (off ^ 16), w[i][1]);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t r = r0 + (i & 2);
+                const uint32_t dst = stage + ((i & 1) ^ odd) * slice + r * 128 + ((2 * (lane & 3) ^ r) << 4);
+                st_smem_v4(dst, w[i][0]);
+                st_smem_v4(dst ^ 16, w[i][1]);
             }
-            fence_proxy_async_smem();
-            // one warp's report covers the RoPE slice
-            if (!v && lw == 0 && !warp_wait(&bar_kst[t & 1], static_cast<uint32_t>(t >> 1 & 1), wc, kErrLatWait | 3)) break;
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(full);
+            if (q & 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
+            }
         }
     } else if (!kQ8 && (warp == kKWarp0 || warp == kVWarp0)) {
         // ------------------------------------------ bf16 operands reported (and cleaned)
@@ -503,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         const uint32_t full = mapa_u32(smem_u32(v ? &bar_vfull[0] : &bar_kfull[0]), 0);
         for (int t = 0; t < nt; ++t) {
             const int st = t & 1;
-            if (!warp_wait(&landed[st], static_cast<uint32_t>(t >> 1 & 1), wc, kErrLatWait | 13)) break;
+            if (!wait(&landed[st], static_cast<uint32_t>(t >> 1 & 1), 13)) break;
             const int tile0 = (t0 + t) * kNK;
             if (v && tile0 + kNK > it.past) {  // lane = 16-byte piece of a row
                 for (int j = max(0, it.past - tile0); j < kNK; ++j) {
@@ -528,27 +619,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             bool ok = true;
             for (int t = 0; t <= nt; ++t) {
                 if (t < nt) {  // scores(t)
-                    const int st = t % kStages, sb = t & 1;
-                    ok = warp_spin(&bar_kfull[st], static_cast<uint32_t>(t / kStages & 1), wc, kErrLatWait | 3) &&
-                         (t < 2 || warp_spin(&bar_sfree[sb], static_cast<uint32_t>(t >> 1 & 1) ^ 1, wc, kErrLatWait | 4));
+                    const int sb = t & 1;
+                    ok = wait(&bar_kfull[sb], static_cast<uint32_t>(t >> 1 & 1), 3) &&
+                         (t < 2 || wait(&bar_sfree[sb], static_cast<uint32_t>(t >> 1 & 1) ^ 1, 4));
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t kd = kd0 + static_cast<uint32_t>(st * (8 * kKSlice >> 4));
-                    const uint64_t rd = rd0 + static_cast<uint32_t>(sb * (kKSlice >> 4));
+                    const uint64_t kd = kd0 + static_cast<uint32_t>(sb * (8 * kKSlice >> 4));
+                    const uint64_t rd = rd0 + static_cast<uint32_t>(t % S::kRope * (kKSlice >> 4));
                     const uint32_t sc = tmem + kColS + 32 * sb;
                     if (elect_one()) {
+#pragma unroll 1
+                        for (int sl = 0; sl < 9; ++sl) {  // 64-dim slices, 16 dims each
+                            const uint64_t qs = qd + sl * (kQSlice >> 4), ks = sl < 8 ? kd + sl * (kKSlice >> 4) : rd;
 #pragma unroll
-                        for (int i = 0; i < 36; ++i)  // 64-dim slice i / 4, 16 dims each
-                            mma_bf16_pair(sc, qd + (i >> 2) * (kQSlice >> 4) + 2 * (i & 3),
-                                          (i < 32 ? kd + (i >> 2) * (kKSlice >> 4) : rd) + 2 * (i & 3), id_qk, i != 0 ? 1u : 0u);
+                            for (int i = 0; i < 4; ++i) mma_bf16_pair(sc, qs + 2 * i, ks + 2 * i, id_qk, (sl | i) != 0 ? 1u : 0u);
+                        }
                         tc_commit_pair(&bar_s[sb]);
                     }
                     __syncwarp();
                 }
                 if (t > 0) {  // aggregation(t - 1)
-                    const int u = t - 1, st = u % kStages;
-                    ok = warp_spin(&bar_vfull[st], static_cast<uint32_t>(u / kStages & 1), wc, kErrLatWait | 5) &&
-                         warp_spin(&bar_pfull, static_cast<uint32_t>(u & 1), wc, kErrLatWait | 6);
+                    const int u = t - 1, st = u & 1;
+                    ok = wait(&bar_vfull[st], static_cast<uint32_t>(u >> 1 & 1), 5) &&
+                         wait(&bar_pfull, static_cast<uint32_t>(u & 1), 6);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t vd = vd0 + static_cast<uint32_t>(st * (kVStage >> 4));
@@ -563,17 +656,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     __syncwarp();
                 }
             }
-            // every product has finished (fixed limit) before the pair tears down
-            int dummy = 0;
-            WaitCtx dw(a.err, reinterpret_cast<volatile int*>(&dummy), kWaitLimitNs);
             if (elect_one()) tc_commit_pair(&bar_final);
             __syncwarp();
-            if (lane == 0) mbar_wait(&bar_final, 0, dw, kErrLatWait | 7);
-        } else if (lane == 0) {
-            // the last arrival this CTA gets (the even CTA's waits all have limits, so it comes)
-            int dummy = 0;
-            WaitCtx dw(a.err, reinterpret_cast<volatile int*>(&dummy), 4 * kWaitLimitNs);
-            mbar_wait(&bar_final, 0, dw, kErrLatWait | 12);
+        }
+        // every product has finished (fixed limit), and the last arrival this CTA gets has come, before
+        // the pair tears down (the even CTA's waits all have limits)
+        if (lane == 0) {
+            int none = 0;
+            const Waits w{&none, static_cast<uint32_t>(rank ? 4 * kWaitLimitNs : kWaitLimitNs)};
+            if (!w.one(&bar_final, 0, 12)) s_abort = 12;
         }
         __syncwarp();
     }
@@ -586,7 +677,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t sfree0 = mapa_u32(smem_u32(&bar_sfree[0]), 0), pfull0 = mapa_u32(smem_u32(&bar_pfull), 0);
         const uint32_t prow = smem_u32(sm + S::kOffP) + r * 128;
-        const float c2 = a.scale * 1.4426950408889634f;  // scores in base-2 units
+        // scores in base-2 units (the queries carry the sign; never 0, so that masked scores stay -inf)
+        const float c2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         // which of this thread's 32 keys of tile t it attends to.  Selections: the
@@ -619,6 +711,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             uint32_t v = s0 < it.past ? (1u << (it.past - s0)) - 1u : 0u;
             const int n = min(32, it.n_keys - s0);
             const uint8_t* mk = a.tree_mask ? a.tree_mask + (static_cast<int64_t>(it.b) * a.T + token) * a.T : nullptr;
+#pragma unroll 1
             for (int j = max(0, it.past - s0); j < n; ++j) {
                 const int d = s0 + j - it.past;
                 if (mk ? mk[d] != 0 : d <= token) v |= 1u << j;
@@ -626,10 +719,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             return v;
         };
         if (a.idx) load_slots(0);
-        uint32_t vis = nt > 0 ? visible(0) : 0u;
+#pragma unroll 1
         for (int t = 0; t < nt; ++t) {
             const int sb = t & 1;
-            ok = ok && warp_wait(&bar_s[sb], static_cast<uint32_t>((t >> 1) & 1), wc, kErrLatWait | 8);
+            const uint32_t vis = visible(t);
+            ok = ok && wait(&bar_s[sb], static_cast<uint32_t>((t >> 1) & 1), 8);
             float s[32];
             if (ok) {
                 tc_fence_after();
@@ -640,7 +734,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(sfree0 + 8 * sb);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j]) * c2;
+                for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j]);
                 if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -651,7 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 for (int j = 0; j < 32; ++j) s[j] = -INFINITY;
                 if (lane == 0) s_fail[sb] = 1;
             }
-            const float mx = tree_max(s);
+            const float mx = tree_max(s) * c2;
             s_max[sb][tid] = mx;
             named_sync(1, 32 * kSmxWarps);
             // a failed wait before this barrier is seen by all four warps after it (the flag
@@ -661,13 +755,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 break;
             }
             const float top = fmaxf(mx, s_max[sb][tid ^ 64]);
-            if (t + 1 < nt) vis = visible(t + 1);
             const bool grow = top > m + kRescaleLog2;
             if (__any_sync(0xffffffffu, grow)) {
                 const float m_new = grow ? top : m;
                 const float alpha = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - m_new)) : 1.f;
                 if (t > 0) {  // O holds the tiles before t
-                    ok = warp_wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), wc, kErrLatWait | 9);
+                    ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 9);
                     if (ok) {
                         tc_fence_after();
 #pragma unroll 1
@@ -690,14 +783,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             float sum = 0.f;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                const float p0 = fast_exp2(s[2 * j] - mref), p1 = fast_exp2(s[2 * j + 1] - mref);
+                const float p0 = fast_exp2(s[2 * j] * c2 - mref), p1 = fast_exp2(s[2 * j + 1] * c2 - mref);
                 sum += p0 + p1;
                 pk[j] = pack_bf16x2(p0, p1);
             }
             l += sum;
             // aggregation(t - 1) has read P
             if (ok && t > 0)
-                ok = warp_wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), wc, kErrLatWait | 10);
+                ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 10);
             if (ok) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
@@ -714,8 +807,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         named_sync(1, 32 * kSmxWarps);
         l += s_sum[tid ^ 64];
         if (ok && nt > 0)
-            ok = warp_wait(&bar_o[(nt - 1) & 1], static_cast<uint32_t>((nt - 1) >> 1 & 1), wc, kErrLatWait | 11);
-        if (ok && !*wc.abort) {
+            ok = wait(&bar_o[(nt - 1) & 1], static_cast<uint32_t>((nt - 1) >> 1 & 1), 11);
+        if (ok && !*wait.abort) {
             tc_fence_after();
             const bool partial = ka.nsplit > 1;
             const bool bf = !partial && a.out_bf16 != nullptr;
@@ -747,7 +840,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             fence_proxy_async_smem();
         }
         named_sync(1, 32 * kSmxWarps);  // both threads of a row have staged it (one bulk copy per row)
-        if (ok && !*wc.abort && live && hf == 0) {
+        if (ok && !*wait.abort && live && hf == 0) {
             const bool partial = ka.nsplit > 1;
             const int64_t orow = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + m_row;
             const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
@@ -765,6 +858,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && *wait.abort) record_error(a.err, kErrLatWait | *wait.abort);
     cluster_sync_all();  // no more remote arrivals, stores or products in either CTA
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);

@@ -563,13 +563,21 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, uint32_t scale2) {
 }
 
 
-// The same four values in the order 0, 2, 1, 3, which takes fewer shifts: codes
-// 1 and 3 already stand in the upper bytes of the two halves.
-__device__ __forceinline__ uint2 e4m3x4_to_bf16x4_0213(uint32_t w, uint32_t scale2) {
-    constexpr uint32_t k2p120 = 0x7B807B80u;
+// Four e4m3 codes -> four bf16 in the order 0, 2, 1, 3 (codes 1 and 3 already
+// stand in the upper bytes of the two halves, which saves shifts), times a factor
+// that makes up for the fields' 2^-120 (q8_factor_bf16x2).
+__device__ __forceinline__ uint2 e4m3x4_to_bf16x4_0213(uint32_t w, uint32_t factor2) {
     const uint32_t e = ((w << 4) & 0x07F007F0u) | ((w << 8) & 0x80008000u);
     const uint32_t o = ((w >> 4) & 0x07F007F0u) | (w & 0x80008000u);
-    return make_uint2(hmul2_bf16(hmul2_bf16(e, k2p120), scale2), hmul2_bf16(hmul2_bf16(o, k2p120), scale2));
+    return make_uint2(hmul2_bf16(e, factor2), hmul2_bf16(o, factor2));
+}
+// 2^120 times the scale, as far as bf16 reaches: up to the byte 134; a larger one
+// takes a second factor 2^(e-134) (q8_excess_bf16x2; 1 for the others).
+__device__ __forceinline__ uint32_t q8_factor_bf16x2(uint32_t e) {
+    return (e == 255u ? 0x7FC0u : (min(e, 134u) + 120u) << 7) * 0x10001u;
+}
+__device__ __forceinline__ uint32_t q8_excess_bf16x2(uint32_t e) {
+    return ((e == 255u ? 134u : max(e, 134u)) - 7u << 7) * 0x10001u;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
