@@ -18,7 +18,7 @@
 //    pages) are TMA-loaded into the operands.  e4m3 rows are loaded to registers by
 //    eight warps, a tile ahead, turned into bf16 there, exactly, and stored to the
 //    operands, four warps each; one warp resolves their pool rows and scales, one
-//    gathers the RoPE rows by TMA.  Latent dims stand in the order 0, 2, 1, 3 of
+//    reports stored operands.  Latent dims stand in the order 0, 2, 1, 3 of
 //    each four (fewer shifts), in the query and the output columns alike.
 //    Measured and dropped for the e4m3 rows: cp.async into shared memory (its
 //    requests hold up the barrier arrivals between the CTAs: 2000 cycles per
@@ -53,19 +53,17 @@ constexpr int kVStage = 4 * kVSlice;
 constexpr int kSmxWarps = 4, kLoadWarps = 4;  // loading warps of either operand
 constexpr int kKWarp0 = kSmxWarps, kVWarp0 = kKWarp0 + kLoadWarps;
 constexpr int kMmaWarp = kVWarp0 + kLoadWarps;
-constexpr int kTmaWarp = kMmaWarp + 1;      // e4m3: RoPE rows, score operand reported; bf16: every load
-constexpr int kRowWarp = kTmaWarp + 1;      // e4m3: rows resolved
-constexpr int kVReportWarp = kRowWarp + 1;  // e4m3: aggregation operand reported
-constexpr int kThreads = 32 * (kVReportWarp + 1);
+constexpr int kTmaWarp = kMmaWarp + 1;     // bf16: loads; e4m3: rows resolved
+constexpr int kReportWarp = kTmaWarp + 1;  // e4m3: operands reported
+constexpr int kThreads = 32 * (kReportWarp + 1);
 constexpr int kORow = 512 * 4 + 16;  // a staged output row (padded)
 
 template <bool kQ8>
 struct Smem {
-    static constexpr int kRope = kQ8 ? 3 : 2;    // of the RoPE slice
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kOffQ + 9 * kQSlice;
     static constexpr int kOffR = kOffK + 2 * 8 * kKSlice;
-    static constexpr int kOffV = kOffR + kRope * kKSlice;
+    static constexpr int kOffV = kOffR + 2 * kKSlice;
     static constexpr int kOffP = kOffV + 2 * kVStage;
     static constexpr int kEnd = kOffP + kRows * 128;
     static constexpr int kBytes = kEnd + 1024;
@@ -83,8 +81,8 @@ constexpr uint32_t kColS = 256;  // two score buffers of 32 columns
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxSplits = 32;
 
-// Tensor maps of the pools.  e4m3: one whole row a box.  bf16: boxes of 64 elements by 32 and by 64 rows,
-// RoPE keys by 32 rows, 128-byte swizzle.
+// Tensor maps of the bf16 pools: latent rows in boxes of 64 dims by 32 rows (c) and
+// by 64 rows (cv), RoPE keys by 32 rows, 128-byte swizzle.
 struct Maps {
     CUtensorMap c, cv, kr;
 };
@@ -250,19 +248,6 @@ __device__ __forceinline__ void times4(uint4& v, uint32_t f) {
     v = make_uint4(hmul2_bf16(v.x, f), hmul2_bf16(v.y, f), hmul2_bf16(v.z, f), hmul2_bf16(v.w, f));
 }
 
-// Gather 32 rows (lane = row) of `bytes` each to dst on.  Issued by one lane of the
-// converged warp: from divergent lanes a gather takes longer than its 80 cycles.
-__device__ __forceinline__ void gather32(const void* map, uint32_t dst, int bytes, uint32_t bar, int row) {
-#pragma unroll 1
-    for (int g = 0; g < 8; ++g) {
-        int r[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = __shfl_sync(0xffffffffu, row, 4 * g + i);
-        if (elect_one()) tma_gather4(dst + 4 * g * bytes, map, bar, 0, r[0], r[1], r[2], r[3]);
-        __syncwarp();
-    }
-}
-
 // The loads of the last of `issued` tiles, one per stage, have landed (fixed limit).
 __device__ __forceinline__ void drain(int* abort_word, uint64_t* bars, int stages, int issued, int lane) {
     if (lane == 0) {
@@ -289,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     __shared__ uint64_t bar_rows[kRing], bar_rowsfree[kRing];  // e4m3: rows and scale words of a tile's keys
     __shared__ int s_row[kRing][kNK];
     __shared__ uint32_t s_scale[kRing][kNK];
-    __shared__ uint64_t bar_kst[3], bar_vst[2];      // loads straight into an operand have landed (e4m3: RoPE slice)
+    __shared__ uint64_t bar_kst[2], bar_vst[2];      // bf16: an operand's loads have landed
     __shared__ uint64_t bar_kdone[2], bar_vdone[2];        // e4m3: the loading warps have stored an operand
     // a stage is visible to the tensor cores, the scores are read, P is written: waited for by the
     // issuing thread (the even CTA's copies are used)
@@ -320,6 +305,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar_kdone[i], kLoadWarps);
             mbar_init(&bar_vdone[i], kLoadWarps);
+            mbar_init(&bar_kst[i], 1);
             mbar_init(&bar_vst[i], 1);
             mbar_init(&bar_kfull[i], 2);
             mbar_init(&bar_vfull[i], 2);
@@ -327,10 +313,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             mbar_init(&bar_s[i], 1);
             mbar_init(&bar_o[i], 1);
         }
-        for (int i = 0; i < 3; ++i) mbar_init(&bar_kst[i], 1);
         for (int i = 0; i < kRing; ++i) {
-            mbar_init(&bar_rows[i], 2);
-            mbar_init(&bar_rowsfree[i], 2 * kLoadWarps + 1);
+            mbar_init(&bar_rows[i], 2);  // halves
+            mbar_init(&bar_rowsfree[i], 2 * kLoadWarps);
         }
         mbar_init(&bar_pfull, 2 * kSmxWarps);
         mbar_init(&bar_final, 1);
@@ -346,13 +331,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     // keys of a tile whose rows a warp resolves: e4m3: this CTA's half and the partner's; bf16: the first
     Rows<kQ8> keys, others;
     if (warp >= kTmaWarp) {
-        if (warp == kTmaWarp && lane == 0) {
-            if (!kQ8) tma_prefetch_desc(&maps.c);
-            if (!kQ8) tma_prefetch_desc(&maps.cv);
+        if (!kQ8 && warp == kTmaWarp && lane == 0) {
+            tma_prefetch_desc(&maps.c);
+            tma_prefetch_desc(&maps.cv);
             tma_prefetch_desc(&maps.kr);
         }
-        if (warp == (kQ8 ? kRowWarp : kTmaWarp)) keys.start(a, it, nt, t0 * kNK + (kQ8 ? own0 : 0) + lane);
-        if (kQ8 && warp == kRowWarp) others.start(a, it, nt, t0 * kNK + other0 + lane);
+        if (warp == kTmaWarp) keys.start(a, it, nt, t0 * kNK + (kQ8 ? own0 : 0) + lane);
+        if (kQ8 && warp == kTmaWarp) others.start(a, it, nt, t0 * kNK + other0 + lane);
     } else if (warp < kTmaWarp) {
         // the query rows, as the K-major A operand: row r of this CTA, 16-byte piece c of its 72
         // (512 latent dims, then 64 RoPE dims); rows that are not live are zero
@@ -403,35 +388,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     if (nt <= 0) {
         // no keys: fall through (the softmax warps write the empty result)
     } else if (kQ8 && warp == kTmaWarp) {
-        // ------------------------------------------ e4m3: RoPE slice loaded, score operand reported
-        // (a fence in a loading thread would wait for its stores and loads; the operand's bytes are in this
-        // CTA, so the report to the issuing thread orders no more than that)
-        const uint32_t full = mapa_u32(smem_u32(&bar_kfull[0]), 0);
-        int issued = 0;
-#pragma unroll 1
-        for (int t = -2; t < nt; ++t) {
-            if (t >= 0) {
-                if (!wait(&bar_kdone[t & 1], static_cast<uint32_t>(t >> 1 & 1), 1)) break;
-                fence_proxy_async_smem();
-                if (!wait(&bar_kst[t % 3], static_cast<uint32_t>(t / 3 & 1), 2)) break;
-                if (lane == 0) mbar_arrive_remote(full + 8 * (t & 1));
-            }
-            // RoPE slice of tile n (three of them: free once the scores of tile n - 3 are there, so that the
-            // gather never stands between an operand and its report)
-            const int n = t + 2, f = n - 3, st = n % kRing;
-            if (n < nt) {
-                if (f >= 0 && !wait(&bar_s[f & 1], static_cast<uint32_t>(f >> 1 & 1), 3)) break;
-                if (!wait(&bar_rows[st], static_cast<uint32_t>(n / kRing & 1), 4)) break;
-                const int row = s_row[st][own0 + lane];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
-                if (elect_one()) mbar_arrive_expect_tx(&bar_kst[n % 3], kKSlice);
-                gather32(&maps.kr, smem_u32(sm + S::kOffR) + n % 3 * kKSlice, 128, smem_u32(&bar_kst[n % 3]), row);
-                issued = n + 1;
-            }
-        }
-        drain(&s_abort, bar_kst, 3, issued, lane);
-    } else if (kQ8 && warp == kRowWarp) {
         // ------------------------------------------ e4m3: pool rows and scales, as far ahead as the ring goes
 #pragma unroll 1
         for (int h = 0; h < 2 * nt; ++h) {  // half tiles: the lanes' own keys, then the partner's
@@ -448,14 +404,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         }
         if (keys.broken || others.broken) record_error(a.err, kErrMlaIndex);
         __syncwarp();
-    } else if (kQ8 && warp == kVReportWarp) {
-        // ------------------------------------------ e4m3: aggregation operand reported
-        const uint32_t full = mapa_u32(smem_u32(&bar_vfull[0]), 0);
-#pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-            if (!wait(&bar_vdone[t & 1], static_cast<uint32_t>(t >> 1 & 1), 6)) break;
-            fence_proxy_async_smem();
-            if (lane == 0) mbar_arrive_remote(full + 8 * (t & 1));
+    } else if (kQ8 && warp == kReportWarp) {
+        // ------------------------------------------ e4m3: operands made visible and reported, whichever is stored
+        // (a fence in a loading thread would wait for its stores and loads; an operand's bytes are in this
+        // CTA, so the report to the issuing thread orders no more than that)
+        if (lane == 0) {
+            const uint32_t kfull = mapa_u32(smem_u32(&bar_kfull[0]), 0), vfull = mapa_u32(smem_u32(&bar_vfull[0]), 0);
+            int tk = 0, tv = 0;
+            uint32_t since = Waits::now();
+            while (tk < nt || tv < nt) {
+                bool did = false;
+                if (tk < nt && mbar_test_wait(&bar_kdone[tk & 1], static_cast<uint32_t>(tk >> 1 & 1))) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_remote(kfull + 8 * (tk & 1));
+                    ++tk;
+                    did = true;
+                }
+                if (tv < nt && mbar_test_wait(&bar_vdone[tv & 1], static_cast<uint32_t>(tv >> 1 & 1))) {
+                    fence_proxy_async_smem();
+                    mbar_arrive_remote(vfull + 8 * (tv & 1));
+                    ++tv;
+                    did = true;
+                }
+                if (did) {
+                    since = Waits::now();
+                } else {
+                    if (*wait.abort) break;
+                    if (Waits::now() - since > wait.limit_ns) {
+                        *wait.abort = 6;
+                        break;
+                    }
+                }
+            }
         }
         __syncwarp();
     } else if (!kQ8 && warp == kTmaWarp) {
@@ -515,12 +495,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         const int sc_shift = v ? 16 * blk + 8 * static_cast<int>(rank) : 8 * blk;
         const uint32_t slice0 = v ? vbase + 2 * blk * kVSlice + row0 * 128 : kbase + 2 * blk * kKSlice + 8 * lw * 128;
         const uint32_t slice = v ? kVSlice : kKSlice;                      // the next 64 dims
+        const uint32_t rbase = smem_u32(sm + S::kOffR);
         uint64_t* freed = v ? bar_o : bar_s;
         // Two steps per tile, four units each (row 4 step + 2 k + odd, pieces as above); two steps' loads
         // are under way.  Rolled up like this the loop is small enough to stay in the instruction cache
         // beside the other roles' (a body of eight units ran at the pace of instruction fetches).
         struct Step {
             uint4 u[4];
+            uint4 kr;     // scores: piece lane % 8 of the RoPE key of row 4 step + lane / 8
             uint32_t sc;  // scale word of row lane % 8
         };
         auto fetch = [&](int q, Step& x) {
@@ -531,6 +513,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 #pragma unroll
             for (int k = 0; k < 2; ++k) row[k] = s_row[st][row0 + 4 * (q & 1) + 2 * k + odd];
             x.sc = s_scale[st][row0 + (lane & 7)];
+            if (!v) {
+                const int r = s_row[st][row0 + 4 * (q & 1) + (lane >> 3)];
+                x.kr = make_uint4(0u, 0u, 0u, 0u);
+                if (r >= 0) x.kr = ld_row16(static_cast<const __nv_bfloat16*>(a.kr_cache) + r * a.kr_ld + 8 * (lane & 7));
+            }
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const uint8_t* src = src0 + row[k] * a.c_ld;
@@ -570,6 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     times4(w[i][1], f);
                 }
             }
+            const uint4 kr = cur.kr;
             cur = next;
             if (!fetch(q + 2, next)) break;
             const int tf = t - 2;  // the tile whose products free the stage
@@ -581,6 +569,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 const uint32_t dst = stage + ((i & 1) ^ odd) * slice + r * 128 + ((2 * (lane & 3) ^ r) << 4);
                 st_smem_v4(dst, w[i][0]);
                 st_smem_v4(dst ^ 16, w[i][1]);
+            }
+            if (!v) {
+                const int r = 8 * lw + 4 * (q & 1) + (lane >> 3);
+                st_smem_v4(rbase + (t & 1) * kKSlice + r * 128 + (((lane & 7) ^ (r & 7)) << 4), kr);
             }
             if (q & 1) {
                 __syncwarp();
@@ -625,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t kd = kd0 + static_cast<uint32_t>(sb * (8 * kKSlice >> 4));
-                    const uint64_t rd = rd0 + static_cast<uint32_t>(t % S::kRope * (kKSlice >> 4));
+                    const uint64_t rd = rd0 + static_cast<uint32_t>(sb * (kKSlice >> 4));
                     const uint32_t sc = tmem + kColS + 32 * sb;
                     if (elect_one()) {
 #pragma unroll 1
@@ -939,18 +931,17 @@ size_t state_bytes(int64_t items, int ns) { return static_cast<size_t>(items) * 
 template <bool kQ8>
 sa_status launch(const Args& ka, int64_t items, cudaStream_t st) {
     const LatentArgs& a = ka.a;
-    const uint64_t rows = static_cast<uint64_t>(a.pool_pages) * kPage;
     Maps maps = {};
-    const uint64_t dims[2] = {kQ8 ? 256u : 512u, rows}, rdims[2] = {64, rows};  // (e4m3: pairs of codes)
-    const uint64_t stride[1] = {static_cast<uint64_t>(a.c_ld) * (kQ8 ? 1 : 2)}, rstride[1] = {static_cast<uint64_t>(a.kr_ld) * 2};
-    const uint32_t box[2] = {kQ8 ? 256u : 64u, kQ8 ? 1u : 32u}, vbox[2] = {64u, 64u};
-    const uint32_t rbox[2] = {64u, kQ8 ? 1u : 32u};
-    const CUtensorMapDataType dt = kQ8 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const CUtensorMapSwizzle swz = kQ8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;  // of latent rows
-    if (!encode_tiled(&maps.c, dt, 2, a.c_cache, dims, stride, box, swz) ||
-        (!kQ8 && !encode_tiled(&maps.cv, dt, 2, a.c_cache, dims, stride, vbox, swz)) ||
-        !encode_tiled(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kr_cache, rdims, rstride, rbox, CU_TENSOR_MAP_SWIZZLE_128B))
-        return SA_ECUDA;
+    if (!kQ8) {
+        const uint64_t rows = static_cast<uint64_t>(a.pool_pages) * kPage;
+        const uint64_t dims[2] = {512, rows}, rdims[2] = {64, rows};
+        const uint64_t stride[1] = {static_cast<uint64_t>(a.c_ld) * 2}, rstride[1] = {static_cast<uint64_t>(a.kr_ld) * 2};
+        const uint32_t half[2] = {64, kOwn}, whole[2] = {64, kNK};
+        if (!encode_tiled(&maps.c, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c_cache, dims, stride, half, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_tiled(&maps.cv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.c_cache, dims, stride, whole, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode_tiled(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kr_cache, rdims, rstride, half, CU_TENSOR_MAP_SWIZZLE_128B))
+            return SA_ECUDA;
+    }
     const cudaError_t e = cudaFuncSetAttribute(mla_latent_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kQ8>::kBytes);
     if (e != cudaSuccess) return launch_status(e);
     mla_latent_kernel<kQ8><<<static_cast<unsigned>(2 * items * ka.nsplit), kThreads, Smem<kQ8>::kBytes, st>>>(ka, maps);

@@ -234,17 +234,6 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* map, uint64_t
         : "memory");
 }
 
-// Four rows of a 2D tensor (box one row high) at column x, landing one after the
-// other; a row outside the tensor reads as zeros.
-__device__ __forceinline__ void tma_gather4(uint32_t dst, const void* map, uint32_t bar, int x, int r0, int r1, int r2,
-                                            int r3) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, "
-        "%5, %6, %7}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
-        : "memory");
-}
-
 // Contiguous global -> shared bulk copy into this CTA's shared memory,
 // completing `bytes` transactions on `bar`.  Both addresses 16-byte aligned,
 // bytes a multiple of 16.
