@@ -110,11 +110,12 @@ def lib():
 
 
 def _p(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # current_stream() builds a Stream object: 3.2 us a call against 0.3
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(fn: str, st: int):
@@ -457,11 +458,12 @@ def _need(t, name: str, dtypes, shape=None, contiguous=True):
     """Check one tensor argument: on the current device, of an allowed dtype,
     of the given shape (None: any extent) and, unless strides are passed on,
     contiguous."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape))):
+    if shape is not None and t.shape != shape and (
+            t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape))):
         raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
                          f"not {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
@@ -483,10 +485,12 @@ def _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_ro
         raise ValueError(f"the cache holds whole pages of 64 rows, not {n} rows")
     _need(c_cache, "c_cache", (torch.float8_e4m3fn, torch.bfloat16), (n, 512), contiguous=False)
     _need(kr_cache, "kr_cache", (torch.bfloat16,), (n, 64), contiguous=False)
-    pools = [c_cache, kr_cache]
+    (c_ld, one), (kr_ld, one_kr), s_ld = c_cache.stride(), kr_cache.stride(), 0
     if quantised:
-        pools.append(_need(c_scale, "c_scale", _SCALE_TYPES, (n, 4), contiguous=False))
-    if any(t.stride(1) != 1 for t in pools):
+        _need(c_scale, "c_scale", _SCALE_TYPES, (n, 4), contiguous=False)
+        s_ld, one_s = c_scale.stride()
+        one *= one_s
+    if one != 1 or one_kr != 1:
         raise ValueError("the dims of a cache row must be contiguous")
     if page_table is not None:
         _need(page_table, "page_table", (torch.int32,), (None, pages_per_seq))
@@ -494,13 +498,25 @@ def _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_ro
         _need(seq_of_row, "seq_of_row", (torch.int32,), (rows,))
     elif page_table is not None and page_table.shape[0] < rows:
         raise ValueError(f"page_table has {page_table.shape[0]} sequences for {rows} rows")
-    return (SA_E4M3 if quantised else SA_BF16, c_cache.stride(0), c_scale.stride(0) if quantised else 0,
-            kr_cache.stride(0), n // 64)
+    return SA_E4M3 if quantised else SA_BF16, c_ld, s_ld, kr_ld, n // 64
 
 
 def _need_tables(cos, sin, half):
     _need(cos, "cos", (torch.float32,), (None, half))
     _need(sin, "sin", (torch.float32,), tuple(cos.shape))
+
+
+def _heads_out(x, out):
+    """Output of per-head rows x [tokens, H, D], made when not given."""
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _need(out, "output", (x.dtype,), x.shape, contiguous=False)
+        if (out.stride(0) == 0 and x.shape[0] > 1) or (out.stride(1) == 0 and x.shape[1] > 1):
+            raise ValueError("an output must not be a broadcast view")
+    if x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+        raise ValueError("the dims of a head must be contiguous")
+    return out
 
 
 def _code(t) -> int:
@@ -516,31 +532,31 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps: f
     halves or interleaved pairs; cos = sin = None: no rotation.  Token and
     head strides are free; q_out and k_out may be q and k.  Returns (q_out, k_out)."""
     tokens, Hq, D = q.shape
-    rope = 0 if cos is None else 2 * cos.shape[1]
-    ins, outs = [_need(q, "q", _IO_TYPES, contiguous=False)], [q_out]
+    _need(q, "q", _IO_TYPES, contiguous=False)
+    q_out = _heads_out(q, q_out)
+    keys = (None, 0, 0, None, 0, 0, 0)
     if k is not None:
-        ins.append(_need(k, "k", (q.dtype,), (tokens, None, D), contiguous=False))
-        outs.append(k_out)
-    for i, (x, o) in enumerate(zip(ins, outs)):
-        outs[i] = torch.empty(x.shape, dtype=x.dtype, device=x.device) if o is None else \
-            _need(o, "output", (x.dtype,), tuple(x.shape), contiguous=False)
-    if any(t.stride(2) != 1 and D > 1 for t in ins + outs):
-        raise ValueError("the dims of a head must be contiguous")
-    if any(t.stride(i) == 0 and t.shape[i] > 1 for t in outs for i in (0, 1)):
-        raise ValueError("an output must not be a broadcast view")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _need(w, name, (torch.float32,), (D,))
+        _need(k, "k", (q.dtype,), (tokens, None, D), contiguous=False)
+        k_out = _heads_out(k, k_out)
+        ks, os = k.stride(), k_out.stride()
+        keys = (k.data_ptr(), ks[0], ks[1], k_out.data_ptr(), os[0], os[1], k.shape[1])
+    else:
+        k_out = None
+    if q_weight is not None:
+        _need(q_weight, "q_weight", (torch.float32,), (D,))
+    if k_weight is not None:
+        _need(k_weight, "k_weight", (torch.float32,), (D,))
+    rope = 0 if cos is None else 2 * cos.shape[1]
     if rope:
         _need_tables(cos, sin, rope // 2)
         _need(positions, "positions", (torch.int32,), (tokens,))
-    side = lambda x, o: (_p(x), x.stride(0), x.stride(1), _p(o), o.stride(0), o.stride(1), x.shape[1])  # noqa: E731
-    keys = (None, 0, 0, None, 0, 0, 0) if k is None else side(ins[1], outs[1])
-    st = lib().sa_qk_norm_rope(*side(ins[0], outs[0]), *keys, _code(q), _p(q_weight), _p(k_weight), int(bool(norm)),
-                               float(eps), _p(cos), _p(sin), cos.shape[0] if rope else 0, _p(positions), tokens, D,
-                               rope_start, rope, int(bool(interleaved)), _stream())
+    qs, os = q.stride(), q_out.stride()
+    st = lib().sa_qk_norm_rope(q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os[0], os[1], Hq, *keys, _code(q),
+                               _p(q_weight), _p(k_weight), int(bool(norm)), float(eps), _p(cos), _p(sin),
+                               cos.shape[0] if rope else 0, _p(positions), tokens, D, rope_start, rope,
+                               int(bool(interleaved)), _stream())
     _check("sa_qk_norm_rope", st)
-    return outs[0], (None if k is None else outs[1])
+    return q_out, k_out
 
 
 def mla_cache_write(c, kr, c_cache, kr_cache, slots, pages_per_seq: int, cos, sin, positions=None, weight=None,
@@ -581,10 +597,12 @@ def mla_cache_read(c_cache, kr_cache, idx, pages_per_seq: int, c_scale=None, pag
     dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
     if c_out is None:
         c_out = torch.empty(rows, k, 512, dtype=torch.bfloat16, device=idx.device)
+    else:
+        _need(c_out, "c_out", (torch.bfloat16,), (rows, k, 512))
     if kr_out is None:
         kr_out = torch.empty(rows, k, 64, dtype=torch.bfloat16, device=idx.device)
-    _need(c_out, "c_out", (torch.bfloat16,), (rows, k, 512))
-    _need(kr_out, "kr_out", (torch.bfloat16,), (rows, k, 64))
+    else:
+        _need(kr_out, "kr_out", (torch.bfloat16,), (rows, k, 64))
     st = lib().sa_mla_cache_read(_p(c_cache), dt, c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld, pool, _p(page_table),
                                  pages_per_seq, _p(seq_of_row), _p(idx), rows, k, 512, 64, _p(c_out), _p(kr_out),
                                  _stream())
@@ -611,7 +629,8 @@ def _latent_io(q_lat, q_rope, out, lse, workspace, need: int):
     _need(q_rope, "q_rope", (torch.bfloat16,), lead + (64,))
     if out is None:
         out = torch.empty(lead + (512,), dtype=torch.float32, device=q_lat.device)
-    _need(out, "out", _IO_TYPES, lead + (512,))
+    else:
+        _need(out, "out", _IO_TYPES, lead + (512,))
     if lse is not None:
         _need(lse, "lse", (torch.float32,), lead)
     if workspace is None and need:

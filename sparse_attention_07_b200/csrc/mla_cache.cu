@@ -148,20 +148,23 @@ __global__ void __launch_bounds__(kThreads) mla_cache_write_kernel(const CacheWr
     }
 }
 
-// Warp = four slots of one row.
+// Warp = kSlots consecutive slots of the flat [rows * k] index array.
+constexpr int kSlots = 4;
 template <bool kQ8>
 __global__ void __launch_bounds__(kThreads) mla_cache_read_kernel(const CacheReadArgs a) {
     const int lane = threadIdx.x & 31;
-    const int64_t quads = (static_cast<int64_t>(a.k) + 3) / 4;
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (item >= quads * a.rows) return;
-    const int r = static_cast<int>(item / quads);
-    const int64_t j0 = item % quads * 4;
-    const int seq = a.seq_of_row ? a.seq_of_row[r] : r;
-    int64_t row = -1;  // lane i < 4: slot j0 + i
-    if (lane < 4 && j0 + lane < a.k) {
-        const int p = a.idx[static_cast<int64_t>(r) * a.k + j0 + lane];
+    const int64_t total = static_cast<int64_t>(a.rows) * a.k;
+    const int64_t o0 = (static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5)) * kSlots;
+    if (o0 >= total) return;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kSlots), total - o0));
+    int64_t row = -1;  // lane i < kSlots: slot o0 + i
+    if (lane < n) {
+        const int64_t o = o0 + lane;
+        const int p = a.idx[o];
         if (p >= 0) {
+            // a 64-bit division only where the count needs one
+            const int r = static_cast<int>(total >> 32 ? o / a.k : static_cast<uint32_t>(o) / static_cast<uint32_t>(a.k));
+            const int seq = a.seq_of_row ? a.seq_of_row[r] : r;
             row = cache_row(a.page_table, a.pages_per_seq, a.pool_pages, seq, p);
             if (row < 0) {
                 record_error(a.err, kErrMlaIndex);
@@ -169,12 +172,11 @@ __global__ void __launch_bounds__(kThreads) mla_cache_read_kernel(const CacheRea
             }
         }
     }
-    const int n = static_cast<int>(min(static_cast<int64_t>(4), a.k - j0));
     constexpr int kPieces = kQ8 ? 1 : 2;
-    uint4 u[4][kPieces];
-    uint32_t sc[4];
+    uint4 u[kSlots][kPieces];
+    uint32_t sc[kSlots];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
         const int64_t ri = __shfl_sync(0xffffffffu, row, i);
         sc[i] = 0;
 #pragma unroll
@@ -195,10 +197,9 @@ __global__ void __launch_bounds__(kThreads) mla_cache_read_kernel(const CacheRea
     uint4 kr = make_uint4(0u, 0u, 0u, 0u);
     if (rk >= 0)
         kr = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kr_cache) + rk * a.kr_ld + (lane & 7) * 8);
-    const int64_t o0 = static_cast<int64_t>(r) * a.k + j0;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.c_out) + o0 * kDc;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kSlots; ++i) {
         if (i >= n) break;
         if (kQ8) {
             const uint32_t s2 = q8_scale_bf16x2(sc[i]);
@@ -228,8 +229,8 @@ sa_status mla_cache_write_launch(const CacheWriteArgs& a, sa_dtype dt, cudaStrea
 }
 
 sa_status mla_cache_read_launch(const CacheReadArgs& a, cudaStream_t st) {
-    const int64_t warps = (static_cast<int64_t>(a.k) + 3) / 4 * a.rows;
-    const int64_t blocks = (warps + 3) / 4;
+    constexpr int64_t kPerBlock = kThreads / 32 * kSlots;
+    const int64_t blocks = (static_cast<int64_t>(a.rows) * a.k + kPerBlock - 1) / kPerBlock;
     if (blocks > 0x7FFFFFFF) return SA_EUNSUPPORTED;
     if (a.c_scale)
         mla_cache_read_kernel<true><<<static_cast<unsigned>(blocks), kThreads, 0, st>>>(a);

@@ -73,11 +73,11 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
     const uint32_t nq = (a.Hq + kHeads - 1) / kHeads, nk = (a.Hk + kHeads - 1) / kHeads, parts = nq + nk;
     const uint64_t item = (static_cast<uint64_t>(blockIdx.x) * kThreads + threadIdx.x) >> lg_group;
     const int l = threadIdx.x & ((1 << lg_group) - 1);
-    // a 64-bit division only where the count needs one
-    const uint64_t tok = item >> 32 ? item / parts : static_cast<uint32_t>(item) / parts;
-    const bool in = tok < static_cast<uint64_t>(a.tokens) && l < lanes;
+    // the caller has checked that tokens * heads <= 2^32: a 32-bit division serves
+    const uint32_t tok = static_cast<uint32_t>(item) / parts;
+    const bool in = item >> 32 == 0 && tok < static_cast<uint32_t>(a.tokens) && l < lanes;
     const int token = in ? static_cast<int>(tok) : 0;
-    const uint32_t part = in ? static_cast<uint32_t>(item - tok * parts) : 0;
+    const uint32_t part = in ? static_cast<uint32_t>(item) - tok * parts : 0;
     const bool is_k = part >= nq;
     const int h0 = static_cast<int>(is_k ? part - nq : part) * kHeads;
     const int n = in ? (is_k ? a.Hk : a.Hq) - h0 : 0;  // heads left for this group
