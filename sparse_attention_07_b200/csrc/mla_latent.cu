@@ -50,12 +50,12 @@ constexpr int kOwn = 32;   // keys of a tile that one CTA loads
 constexpr int kRows = 64;  // query rows per CTA
 constexpr int kQSlice = kRows * 128, kKSlice = kOwn * 128, kVSlice = kNK * 128;  // 64 dims each
 constexpr int kVStage = 4 * kVSlice;
-constexpr int kSmxWarps = 4, kLoadWarps = 4;  // loading warps of either operand
+constexpr int kSmxWarps = 4, kLoadWarps = 8;  // loading warps of either operand
 constexpr int kKWarp0 = kSmxWarps, kVWarp0 = kKWarp0 + kLoadWarps;
 constexpr int kMmaWarp = kVWarp0 + kLoadWarps;
 constexpr int kTmaWarp = kMmaWarp + 1;     // bf16: loads; e4m3: rows resolved
-constexpr int kReportWarp = kTmaWarp + 1;  // e4m3: operands reported
-constexpr int kThreads = 32 * (kReportWarp + 1);
+constexpr int kReportWarp = kTmaWarp + 1;  // e4m3: stored operands reported, scores' and aggregation's
+constexpr int kThreads = 32 * (kReportWarp + 2);
 constexpr int kORow = 512 * 4 + 16;  // a staged output row (padded)
 
 template <bool kQ8>
@@ -124,6 +124,7 @@ struct Waits {
     }
     // The whole warp leaves together.
     __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity, int site) const {
+        if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
         int ok = 1;
         if ((threadIdx.x & 31) == 0) ok = one(b, parity, site) ? 1 : 0;
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
@@ -267,6 +268,8 @@ __device__ __forceinline__ bool bad4(uint4 v) {
 template <bool kQ8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_latent_kernel(const Args ka, const __grid_constant__ Maps maps) {
     pdl_trigger();
+    // Registers: the softmax holds 32 scores a thread, the other roles less (the sum is the launch's).
+    static_assert(kThreads == 768, "six warpgroups of 80 registers a thread");
     using S = Smem<kQ8>;
     const LatentArgs& a = ka.a;
     extern __shared__ uint8_t smem_raw[];
@@ -404,37 +407,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         }
         if (keys.broken || others.broken) record_error(a.err, kErrMlaIndex);
         __syncwarp();
-    } else if (kQ8 && warp == kReportWarp) {
-        // ------------------------------------------ e4m3: operands made visible and reported, whichever is stored
+    } else if (kQ8 && warp >= kReportWarp) {
+        // ------------------------------------------ e4m3: operands made visible and reported as they are stored
         // (a fence in a loading thread would wait for its stores and loads; an operand's bytes are in this
         // CTA, so the report to the issuing thread orders no more than that)
         if (lane == 0) {
-            const uint32_t kfull = mapa_u32(smem_u32(&bar_kfull[0]), 0), vfull = mapa_u32(smem_u32(&bar_vfull[0]), 0);
-            int tk = 0, tv = 0;
-            uint32_t since = Waits::now();
-            while (tk < nt || tv < nt) {
-                bool did = false;
-                if (tk < nt && mbar_test_wait(&bar_kdone[tk & 1], static_cast<uint32_t>(tk >> 1 & 1))) {
-                    fence_proxy_async_smem();
-                    mbar_arrive_remote(kfull + 8 * (tk & 1));
-                    ++tk;
-                    did = true;
-                }
-                if (tv < nt && mbar_test_wait(&bar_vdone[tv & 1], static_cast<uint32_t>(tv >> 1 & 1))) {
-                    fence_proxy_async_smem();
-                    mbar_arrive_remote(vfull + 8 * (tv & 1));
-                    ++tv;
-                    did = true;
-                }
-                if (did) {
-                    since = Waits::now();
-                } else {
-                    if (*wait.abort) break;
-                    if (Waits::now() - since > wait.limit_ns) {
-                        *wait.abort = 6;
-                        break;
-                    }
-                }
+            const bool v = warp != kReportWarp;
+            uint64_t* done = v ? bar_vdone : bar_kdone;
+            const uint32_t full = mapa_u32(smem_u32(v ? &bar_vfull[0] : &bar_kfull[0]), 0);
+#pragma unroll 1
+            for (int t = 0; t < nt; ++t) {
+                if (!wait.one(&done[t & 1], static_cast<uint32_t>(t >> 1 & 1), 6)) break;
+                fence_proxy_async_smem();
+                mbar_arrive_remote(full + 8 * (t & 1));
             }
         }
         __syncwarp();
@@ -480,41 +465,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             drain(&s_abort, bar_vst, 2, issued_v, lane);
         }
     } else if (kQ8 && warp >= kKWarp0 && warp < kMmaWarp) {
-        // ------------------------------------------ e4m3 rows into an operand.  Scores: own rows 8 lw ..
-        // 8 lw + 7 of a tile, 32 pieces of 16 dims each; aggregation: rows 16 lw .. 16 lw + 7 of it in the
-        // lower half warp, 16 lw + 8 .. in the upper, the 16 pieces of this CTA's 256 dims each.  Unit i of a
+        // ------------------------------------------ e4m3 rows into an operand.  Scores: own rows 4 lw ..
+        // 4 lw + 3 of a tile, 32 pieces of 16 dims each; aggregation: rows 8 lw .. 8 lw + 3 of it in the
+        // lower half warp, 8 lw + 4 .. in the upper, the 16 pieces of this CTA's 256 dims each.  Unit i of a
         // lane: of row 2 (i / 2) + odd, odd = lane / 4 % 2, piece 8 (lane / 8) + lane % 4 (+ 4 where i + odd
         // is odd): the eight lanes of a load or store phase touch distinct banks, lanes 0 .. 3 in an even
         // row, lanes 4 .. 7 in the odd one next to it (its swizzle differs in the lowest bit).
         const bool v = warp >= kVWarp0;
         const int lw = warp - (v ? kVWarp0 : kKWarp0), odd = lane >> 2 & 1;
-        const int row0 = v ? 16 * lw + 8 * (lane >> 4) : own0 + 8 * lw;    // of the tile
+        const int row0 = v ? 8 * lw + 4 * (lane >> 4) : own0 + 4 * lw;     // of the tile
         const int blk = v ? lane >> 3 & 1 : lane >> 3;                     // 128-dim block of the lane's pieces
         // unit 0's bytes of row 0, had the lane an even row
         const uint8_t* src0 = static_cast<const uint8_t*>(a.c_cache) + (v ? 256 * blk + 128 * rank : 128 * blk) + 16 * (lane & 3);
         const int sc_shift = v ? 16 * blk + 8 * static_cast<int>(rank) : 8 * blk;
-        const uint32_t slice0 = v ? vbase + 2 * blk * kVSlice + row0 * 128 : kbase + 2 * blk * kKSlice + 8 * lw * 128;
         const uint32_t slice = v ? kVSlice : kKSlice;                      // the next 64 dims
-        const uint32_t rbase = smem_u32(sm + S::kOffR);
+        // where row `odd`'s unit of the lower slice goes: an atom of eight rows, a row in it
+        const uint32_t atom = v ? 8 * lw : 8 * (lw >> 1), r_in = (v ? 4 * (lane >> 4) : 4 * (lw & 1)) + odd;
+        const uint32_t dst0 = (v ? vbase : kbase) + 2 * blk * slice + atom * 128 + r_in * 128 + ((2 * (lane & 3) ^ r_in) << 4);
+        const uint32_t stage = v ? kVStage : 8 * kKSlice;
+        const int rr = 4 * lw + (lane >> 3);  // own row whose RoPE piece lane % 8 this lane moves (scores)
+        const uint32_t rdst = smem_u32(sm + S::kOffR) + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4);
         uint64_t* freed = v ? bar_o : bar_s;
-        // Two steps per tile, four units each (row 4 step + 2 k + odd, pieces as above); two steps' loads
-        // are under way.  Rolled up like this the loop is small enough to stay in the instruction cache
-        // beside the other roles' (a body of eight units ran at the pace of instruction fetches).
+        // The loads of two tiles are under way.
         struct Step {
             uint4 u[4];
-            uint4 kr;     // scores: piece lane % 8 of the RoPE key of row 4 step + lane / 8
-            uint32_t sc;  // scale word of row lane % 8
+            uint4 kr;        // scores: the RoPE piece
+            uint32_t sc[2];  // scale bytes of rows odd and 2 + odd
         };
-        auto fetch = [&](int q, Step& x) {
-            if (q >= 2 * nt) return true;
-            const int t = q >> 1, st = t % kRing;
-            if ((q & 1) == 0 && !wait(&bar_rows[st], static_cast<uint32_t>(t / kRing & 1), 7)) return false;
+        auto fetch = [&](int t, Step& x) {
+            if (t >= nt) return true;
+            const int st = t % kRing;
+            if (!wait(&bar_rows[st], static_cast<uint32_t>(t / kRing & 1), 7)) return false;
             int row[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) row[k] = s_row[st][row0 + 4 * (q & 1) + 2 * k + odd];
-            x.sc = s_scale[st][row0 + (lane & 7)];
+            for (int k = 0; k < 2; ++k) {
+                row[k] = s_row[st][row0 + 2 * k + odd];
+                x.sc[k] = s_scale[st][row0 + 2 * k + odd];
+            }
             if (!v) {
-                const int r = s_row[st][row0 + 4 * (q & 1) + (lane >> 3)];
+                const int r = s_row[st][own0 + rr];
                 x.kr = make_uint4(0u, 0u, 0u, 0u);
                 if (r >= 0) x.kr = ld_row16(static_cast<const __nv_bfloat16*>(a.kr_cache) + r * a.kr_ld + 8 * (lane & 7));
             }
@@ -526,58 +515,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     x.u[2 * k] = ld_row16(src + 64 * odd);
                     x.u[2 * k + 1] = ld_row16(src + 64 * (odd ^ 1));
                 }
+                x.sc[k] = x.sc[k] >> sc_shift & 255u;
             }
-            if (q & 1) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
-            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
             return true;
         };
         Step cur, next;
         bool ok = fetch(0, cur) && fetch(1, next);
 #pragma unroll 1
-        for (int q = 0; ok && q < 2 * nt; ++q) {
-            const int t = q >> 1, r0 = 4 * (q & 1) + odd;
+        for (int t = 0; ok && t < nt; ++t) {
+            const int tf = t - 2;  // the tile whose products free the stage
+            if (tf >= 0 && !wait(&freed[tf & 1], static_cast<uint32_t>(tf >> 1 & 1), 8)) break;
             // a drafted row's non-finite block (byte 255) stays out of the aggregation: its finite codes times 0
             const int drafted_from = v && a.tree ? it.past - (t0 + t) * kNK - row0 : kNK;
-            uint4 w[4][2];
-            uint32_t big = 0;
+            const uint32_t at = dst0 + (t & 1) * stage;
+            const bool big = __any_sync(0xffffffffu, (cur.sc[0] | cur.sc[1]) > 127u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t e = __shfl_sync(0xffffffffu, cur.sc, (lane & 16) + r0 + (i & 2)) >> sc_shift & 255u;
-                const bool hide = e == 255u && r0 + (i & 2) >= drafted_from;
-                convert16(cur.u[i], hide ? 0u : q8_factor_bf16x2(e), w[i][0], w[i][1]);
-                big |= e;
-            }
-            if (__any_sync(0xffffffffu, big > 127u)) {  // scales of 2 and above: some may need a second factor
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t e = cur.sc[k];
+                const bool hide = e == 255u && 2 * k + odd >= drafted_from;
+                const uint32_t f = hide ? 0u : q8_factor_bf16x2(e);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t f = q8_excess_bf16x2(__shfl_sync(0xffffffffu, cur.sc, (lane & 16) + r0 + (i & 2)) >> sc_shift & 255u);
-                    times4(w[i][0], f);
-                    times4(w[i][1], f);
+                for (int i = 0; i < 2; ++i) {
+                    uint4 lo, hi;
+                    convert16(cur.u[2 * k + i], f, lo, hi);
+                    if (big) {  // scales of 2 and above: some may need a second factor
+                        const uint32_t f2 = q8_excess_bf16x2(e);
+                        times4(lo, f2);
+                        times4(hi, f2);
+                    }
+                    // (row + 2: the swizzle's second bit)
+                    const uint32_t dst = ((at + k * 256) ^ (k << 5)) + (i ^ odd) * slice;
+                    st_smem_v4(dst, lo);
+                    st_smem_v4(dst ^ 16, hi);
                 }
             }
-            const uint4 kr = cur.kr;
+            if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, cur.kr);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
             cur = next;
-            if (!fetch(q + 2, next)) break;
-            const int tf = t - 2;  // the tile whose products free the stage
-            if ((q & 1) == 0 && tf >= 0 && !wait(&freed[tf & 1], static_cast<uint32_t>(tf >> 1 & 1), 8)) break;
-            const uint32_t stage = slice0 + (t & 1) * (v ? kVStage : 8 * kKSlice);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t r = r0 + (i & 2);
-                const uint32_t dst = stage + ((i & 1) ^ odd) * slice + r * 128 + ((2 * (lane & 3) ^ r) << 4);
-                st_smem_v4(dst, w[i][0]);
-                st_smem_v4(dst ^ 16, w[i][1]);
-            }
-            if (!v) {
-                const int r = 8 * lw + 4 * (q & 1) + (lane >> 3);
-                st_smem_v4(rbase + (t & 1) * kKSlice + r * 128 + (((lane & 7) ^ (r & 7)) << 4), kr);
-            }
-            if (q & 1) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
-            }
+            ok = fetch(t + 2, next);
         }
     } else if (!kQ8 && (warp == kKWarp0 || warp == kVWarp0)) {
         // ------------------------------------------ bf16 operands reported (and cleaned)
