@@ -486,7 +486,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         const int rr = 4 * lw + (lane >> 3);  // own row whose RoPE piece lane % 8 this lane moves (scores)
         const uint32_t rdst = smem_u32(sm + S::kOffR) + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4);
         uint64_t* freed = v ? bar_o : bar_s;
-        // The loads of two tiles are under way.
+        // The next tile's loads are under way during a tile's wait; a second tile ahead in registers gained nothing.
         struct Step {
             uint4 u[4];
             uint4 kr;        // scores: the RoPE piece
@@ -521,8 +521,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
             return true;
         };
-        Step cur, next;
-        bool ok = fetch(0, cur) && fetch(1, next);
+        Step cur;
+        bool ok = fetch(0, cur);
 #pragma unroll 1
         for (int t = 0; ok && t < nt; ++t) {
             const int tf = t - 2;  // the tile whose products free the stage
@@ -554,8 +554,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, cur.kr);
             __syncwarp();
             if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
-            cur = next;
-            ok = fetch(t + 2, next);
+            ok = fetch(t + 1, cur);
         }
     } else if (!kQ8 && (warp == kKWarp0 || warp == kVWarp0)) {
         // ------------------------------------------ bf16 operands reported (and cleaned)
