@@ -50,7 +50,7 @@ constexpr int kOwn = 32;   // keys of a tile that one CTA loads
 constexpr int kRows = 64;  // query rows per CTA
 constexpr int kQSlice = kRows * 128, kKSlice = kOwn * 128, kVSlice = kNK * 128;  // 64 dims each
 constexpr int kVStage = 4 * kVSlice;
-constexpr int kSmxWarps = 4, kLoadWarps = 8;  // loading warps of either operand
+constexpr int kSmxWarps = 8, kLoadWarps = 8;  // loading warps of either operand
 constexpr int kKWarp0 = kSmxWarps, kVWarp0 = kKWarp0 + kLoadWarps;
 constexpr int kMmaWarp = kVWarp0 + kLoadWarps;
 constexpr int kTmaWarp = kMmaWarp + 1;     // bf16: loads; e4m3: rows resolved
@@ -268,8 +268,6 @@ __device__ __forceinline__ bool bad4(uint4 v) {
 template <bool kQ8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_latent_kernel(const Args ka, const __grid_constant__ Maps maps) {
     pdl_trigger();
-    // Registers: the softmax holds 32 scores a thread, the other roles less (the sum is the launch's).
-    static_assert(kThreads == 768, "six warpgroups of 80 registers a thread");
     using S = Smem<kQ8>;
     const LatentArgs& a = ka.a;
     extern __shared__ uint8_t smem_raw[];
@@ -285,8 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     // arrived on in both CTAs when a product is done: scores(t) -> bar_s[t & 1] (K stage free, scores
     // readable), aggregation(t) -> bar_o[t & 1] (V stage and P free, O updated)
     __shared__ uint64_t bar_s[2], bar_o[2], bar_final;
-    __shared__ float s_max[2][128];
-    __shared__ float s_sum[128];
+    __shared__ float s_max[2][32 * kSmxWarps];
+    __shared__ float s_sum[32 * kSmxWarps];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ volatile int s_fail[2];
@@ -639,18 +637,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     }
     if (warp < kSmxWarps) {
         // ---------------------------------------------- softmax + output
-        const int r = tid & 63, hf = tid >> 6;  // row of this CTA, half of the keys (and of the output dims)
+        // row of this CTA; the row's half of the keys (and of the output dims), by tensor-memory lane; quarter of them
+        const int r = tid & 63, hf = tid >> 6 & 1, qd = tid >> 7;
         const int m_row = static_cast<int>(rank) * kRows + r;
         const bool live = m_row < it.tokens * a.H;
         const int token = it.i0 + (live ? m_row / a.H : 0);
-        const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t sfree0 = mapa_u32(smem_u32(&bar_sfree[0]), 0), pfull0 = mapa_u32(smem_u32(&bar_pfull), 0);
         const uint32_t prow = smem_u32(sm + S::kOffP) + r * 128;
         // scores in base-2 units (the queries carry the sign; never 0, so that masked scores stay -inf)
         const float c2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        // which of this thread's 32 keys of tile t it attends to.  Selections: the
+        // which of the 32 keys of this thread's half of tile t its row attends to.  Selections: the
         // slots of eight tiles are loaded eight tiles ahead (the fence that
         // publishes P waits for loads in flight); lane u holds tile u's mask.
         int slots[8];
@@ -691,27 +690,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 #pragma unroll 1
         for (int t = 0; t < nt; ++t) {
             const int sb = t & 1;
-            const uint32_t vis = visible(t);
+            const uint32_t vis = visible(t) >> (16 * qd) & 0xFFFFu;
             ok = ok && wait(&bar_s[sb], static_cast<uint32_t>((t >> 1) & 1), 8);
-            float s[32];
+            float s[16];
             if (ok) {
                 tc_fence_after();
-                uint32_t v[32];
-                tmem_ld32(tmem + lane_base + kColS + 32 * sb, v);
+                uint32_t v[16];
+                tmem_ld16(tmem + lane_base + kColS + 32 * sb + 16 * qd, v);
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(sfree0 + 8 * sb);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = __uint_as_float(v[j]);
-                if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) {
+                for (int j = 0; j < 16; ++j) s[j] = __uint_as_float(v[j]);
+                if (!__all_sync(0xffffffffu, vis == 0xFFFFu)) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
+                    for (int j = 0; j < 16; ++j)
                         if (!(vis >> j & 1u)) s[j] = -INFINITY;
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) s[j] = -INFINITY;
+                for (int j = 0; j < 16; ++j) s[j] = -INFINITY;
                 if (lane == 0) s_fail[sb] = 1;
             }
             const float mx = tree_max(s) * c2;
@@ -723,7 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 ok = false;
                 break;
             }
-            const float top = fmaxf(mx, s_max[sb][tid ^ 64]);
+            const float top = fmaxf(fmaxf(mx, s_max[sb][tid ^ 64]), fmaxf(s_max[sb][tid ^ 128], s_max[sb][tid ^ 192]));
             const bool grow = top > m + kRescaleLog2;
             if (__any_sync(0xffffffffu, grow)) {
                 const float m_new = grow ? top : m;
@@ -733,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     if (ok) {
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < 256; c += 32) {
+                        for (int c = 128 * qd; c < 128 * qd + 128; c += 32) {
                             uint32_t o[32];
                             tmem_ld32(tmem + lane_base + kColO + c, o);
                             tmem_ld_wait();
@@ -748,10 +747,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 m = m_new;
             }
             const float mref = m == -INFINITY ? 0.f : m;  // masked keys are -inf and give exactly 0
-            uint32_t pk[16];
+            uint32_t pk[8];
             float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float p0 = fast_exp2(s[2 * j] * c2 - mref), p1 = fast_exp2(s[2 * j + 1] * c2 - mref);
                 sum += p0 + p1;
                 pk[j] = pack_bf16x2(p0, p1);
@@ -762,8 +761,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 10);
             if (ok) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    st_smem_v4(prow + (((4 * hf + q) ^ (r & 7)) << 4),
+                for (int q = 0; q < 2; ++q)
+                    st_smem_v4(prow + (((4 * hf + 2 * qd + q) ^ (r & 7)) << 4),
                                make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -771,10 +770,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 if (lane == 0) mbar_arrive_remote(pfull0);
             }
         }
-        // ---- both halves' sums, then the rows out: staged over the idle operands, bulk copies
+        // ---- the row's sums, then the rows out: staged over the idle operands, bulk copies
         s_sum[tid] = l;
         named_sync(1, 32 * kSmxWarps);
-        l += s_sum[tid ^ 64];
+        l = (s_sum[r] + s_sum[r + 64]) + (s_sum[r + 128] + s_sum[r + 192]);  // (one order in all four)
         if (ok && nt > 0)
             ok = wait(&bar_o[(nt - 1) & 1], static_cast<uint32_t>((nt - 1) >> 1 & 1), 11);
         if (ok && !*wait.abort) {
@@ -785,8 +784,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             const float inv = empty || partial ? 1.f : 1.f / l;
             uint8_t* srow = sm + r * kORow;
 #pragma unroll 1
-            for (int c = 0; c < 256; c += 32) {
-                const int d = (c >> 7) * 256 + hf * 128 + (c & 127);
+            for (int c = 128 * qd; c < 128 * qd + 128; c += 32) {
+                const int d = qd * 256 + hf * 128 + (c & 127);
                 uint32_t o[32];
                 if (nt > 0) {
                     tmem_ld32(tmem + lane_base + kColO + c, o);
@@ -808,8 +807,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             }
             fence_proxy_async_smem();
         }
-        named_sync(1, 32 * kSmxWarps);  // both threads of a row have staged it (one bulk copy per row)
-        if (ok && !*wait.abort && live && hf == 0) {
+        named_sync(1, 32 * kSmxWarps);  // the threads of a row have staged it (one bulk copy per row)
+        if (ok && !*wait.abort && live && tid < kRows) {
             const bool partial = ka.nsplit > 1;
             const int64_t orow = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + m_row;
             const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
