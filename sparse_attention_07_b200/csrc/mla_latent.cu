@@ -19,7 +19,8 @@
 //    eight warps, a tile ahead, turned into bf16 there, exactly, and stored to the
 //    operands, four warps each; one warp resolves their pool rows and scales, one
 //    reports stored operands.  Latent dims stand in the order 0, 2, 1, 3 of
-//    each four (fewer shifts), in the query and the output columns alike.
+//    each four (fewer shifts), and in odd 64-dim slices with neighbouring groups of
+//    eight swapped (banks), in the query and the output columns alike.
 //    Measured and dropped for the e4m3 rows: cp.async into shared memory (its
 //    requests hold up the barrier arrivals between the CTAs: 2000 cycles per
 //    tile), four-row TMA gathers (200 cycles each beside the products, 16 per
@@ -273,8 +274,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     extern __shared__ uint8_t smem_raw[];
     uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t bar_rows[kRing], bar_rowsfree[kRing];  // e4m3: rows and scale words of a tile's keys
-    __shared__ int s_row[kRing][kNK];
-    __shared__ uint32_t s_scale[kRing][kNK];
+    __shared__ __align__(16) int s_row[kRing][kNK];
+    __shared__ __align__(16) uint32_t s_scale[kRing][kNK];
     __shared__ uint64_t bar_kst[2], bar_vst[2];      // bf16: an operand's loads have landed
     __shared__ uint64_t bar_kdone[2], bar_vdone[2];        // e4m3: the loading warps have stored an operand
     // a stage is visible to the tensor cores, the scores are read, P is written: waited for by the
@@ -374,7 +375,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                         v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
                                        __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
                     if (j < 2 || lane < 8)
-                        st_smem_v4(sQ + ((lane >> 3) + 4 * j) * kQSlice + r * 128 + (((lane & 7) ^ (r & 7)) << 4), v);
+                        st_smem_v4(sQ + ((lane >> 3) + 4 * j) * kQSlice + r * 128 + (((lane & 7) ^ (r & 7) ^ (kQ8 && j < 2 ? lane >> 3 & 1 : 0)) << 4), v);
                 }
             }
         }
@@ -464,63 +465,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         }
     } else if (kQ8 && warp >= kKWarp0 && warp < kMmaWarp) {
         // ------------------------------------------ e4m3 rows into an operand.  Scores: own rows 4 lw ..
-        // 4 lw + 3 of a tile, 32 pieces of 16 dims each; aggregation: rows 8 lw .. 8 lw + 3 of it in the
-        // lower half warp, 8 lw + 4 .. in the upper, the 16 pieces of this CTA's 256 dims each.  Unit i of a
-        // lane: of row 2 (i / 2) + odd, odd = lane / 4 % 2, piece 8 (lane / 8) + lane % 4 (+ 4 where i + odd
-        // is odd): the eight lanes of a load or store phase touch distinct banks, lanes 0 .. 3 in an even
-        // row, lanes 4 .. 7 in the odd one next to it (its swizzle differs in the lowest bit).
+        // 4 lw + 3 of a tile, a row of 32 pieces of 16 dims per load; aggregation: rows 8 lw .. 8 lw + 3 of it in
+        // the lower half warp, 8 lw + 4 .. in the upper, the 16 pieces of this CTA's 256 dims.  Loads are
+        // whole 128-byte lines.  A piece becomes two 16-byte ones of the operand, the later one first in odd
+        // 64-dim slices: so the eight lanes of a store phase, which span two slices, touch distinct banks.
         const bool v = warp >= kVWarp0;
-        const int lw = warp - (v ? kVWarp0 : kKWarp0), odd = lane >> 2 & 1;
+        const int lw = warp - (v ? kVWarp0 : kKWarp0);
         const int row0 = v ? 8 * lw + 4 * (lane >> 4) : own0 + 4 * lw;     // of the tile
         const int blk = v ? lane >> 3 & 1 : lane >> 3;                     // 128-dim block of the lane's pieces
-        // unit 0's bytes of row 0, had the lane an even row
-        const uint8_t* src0 = static_cast<const uint8_t*>(a.c_cache) + (v ? 256 * blk + 128 * rank : 128 * blk) + 16 * (lane & 3);
+        const uint8_t* src0 = static_cast<const uint8_t*>(a.c_cache) + (v ? 256 * blk + 128 * rank : 128 * blk) + 16 * (lane & 7);
         const int sc_shift = v ? 16 * blk + 8 * static_cast<int>(rank) : 8 * blk;
-        const uint32_t slice = v ? kVSlice : kKSlice;                      // the next 64 dims
-        // where row `odd`'s unit of the lower slice goes: an atom of eight rows, a row in it
-        const uint32_t atom = v ? 8 * lw : 8 * (lw >> 1), r_in = (v ? 4 * (lane >> 4) : 4 * (lw & 1)) + odd;
-        const uint32_t dst0 = (v ? vbase : kbase) + 2 * blk * slice + atom * 128 + r_in * 128 + ((2 * (lane & 3) ^ r_in) << 4);
+        const uint32_t sl = 2 * blk + (lane >> 2 & 1);                     // 64-dim slice of the lane's pieces
+        const uint32_t atom = v ? 8 * lw : 8 * (lw >> 1), r0 = v ? 4 * (lane >> 4) : 4 * (lw & 1);  // row0 in the operand
+        const uint32_t dst0 = (v ? vbase : kbase) + sl * (v ? kVSlice : kKSlice) + (atom + r0) * 128 +
+                              ((2 * (lane & 3) + (sl & 1) ^ r0) << 4);
         const uint32_t stage = v ? kVStage : 8 * kKSlice;
         const int rr = 4 * lw + (lane >> 3);  // own row whose RoPE piece lane % 8 this lane moves (scores)
         const uint32_t rdst = smem_u32(sm + S::kOffR) + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4);
         uint64_t* freed = v ? bar_o : bar_s;
         // The next tile's loads are under way during a tile's wait; a second tile ahead in registers gained nothing.
-        struct Step {
-            uint4 u[4];
-            uint4 kr;        // scores: the RoPE piece
-            uint32_t sc[2];  // scale bytes of rows odd and 2 + odd
-        };
-        auto fetch = [&](int t, Step& x) {
+        uint4 u[4], kr = make_uint4(0u, 0u, 0u, 0u);
+        int4 row;  // pool rows (-1: none) and scale words of rows row0 .. row0 + 3
+        uint4 sc;
+        auto fetch = [&](int t) {
             if (t >= nt) return true;
             const int st = t % kRing;
             if (!wait(&bar_rows[st], static_cast<uint32_t>(t / kRing & 1), 7)) return false;
-            int row[2];
+            row = *reinterpret_cast<const int4*>(&s_row[st][row0]);
+            sc = *reinterpret_cast<const uint4*>(&s_scale[st][row0]);
+            int rope = 0;
+            if (!v) rope = s_row[st][own0 + rr];
+            // (a slot without a row loads row 0: its scores are masked, its factor in the aggregation is 0)
+            const int rows[4] = {row.x, row.y, row.z, row.w};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                row[k] = s_row[st][row0 + 2 * k + odd];
-                x.sc[k] = s_scale[st][row0 + 2 * k + odd];
-            }
-            if (!v) {
-                const int r = s_row[st][own0 + rr];
-                x.kr = make_uint4(0u, 0u, 0u, 0u);
-                if (r >= 0) x.kr = ld_row16(static_cast<const __nv_bfloat16*>(a.kr_cache) + r * a.kr_ld + 8 * (lane & 7));
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint8_t* src = src0 + row[k] * a.c_ld;
-                x.u[2 * k] = x.u[2 * k + 1] = make_uint4(0u, 0u, 0u, 0u);
-                if (row[k] >= 0) {
-                    x.u[2 * k] = ld_row16(src + 64 * odd);
-                    x.u[2 * k + 1] = ld_row16(src + 64 * (odd ^ 1));
-                }
-                x.sc[k] = x.sc[k] >> sc_shift & 255u;
-            }
+            for (int i = 0; i < 4; ++i)
+                u[i] = ld_row16(src0 + static_cast<uint64_t>(static_cast<uint32_t>(max(rows[i], 0))) * static_cast<uint32_t>(a.c_ld));
+            if (!v)
+                kr = ld_row16(static_cast<const __nv_bfloat16*>(a.kr_cache) + 8 * (lane & 7) +
+                              static_cast<uint64_t>(static_cast<uint32_t>(max(rope, 0))) * static_cast<uint32_t>(a.kr_ld));
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
             return true;
         };
-        Step cur;
-        bool ok = fetch(0, cur);
+        bool ok = fetch(0);
 #pragma unroll 1
         for (int t = 0; ok && t < nt; ++t) {
             const int tf = t - 2;  // the tile whose products free the stage
@@ -528,31 +515,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             // a drafted row's non-finite block (byte 255) stays out of the aggregation: its finite codes times 0
             const int drafted_from = v && a.tree ? it.past - (t0 + t) * kNK - row0 : kNK;
             const uint32_t at = dst0 + (t & 1) * stage;
-            const bool big = __any_sync(0xffffffffu, (cur.sc[0] | cur.sc[1]) > 127u);
+            const bool big = __any_sync(0xffffffffu, ((sc.x | sc.y | sc.z | sc.w) & 0x80808080u) != 0);
+            const int rows[4] = {row.x, row.y, row.z, row.w};
+            const uint32_t scs[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t e = cur.sc[k];
-                const bool hide = e == 255u && 2 * k + odd >= drafted_from;
-                const uint32_t f = hide ? 0u : q8_factor_bf16x2(e);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint4 lo, hi;
-                    convert16(cur.u[2 * k + i], f, lo, hi);
-                    if (big) {  // scales of 2 and above: some may need a second factor
-                        const uint32_t f2 = q8_excess_bf16x2(e);
-                        times4(lo, f2);
-                        times4(hi, f2);
-                    }
-                    // (row + 2: the swizzle's second bit)
-                    const uint32_t dst = ((at + k * 256) ^ (k << 5)) + (i ^ odd) * slice;
-                    st_smem_v4(dst, lo);
-                    st_smem_v4(dst ^ 16, hi);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t e = scs[i] >> sc_shift & 255u;
+                const bool hide = rows[i] < 0 || (e == 255u && i >= drafted_from);
+                uint4 lo, hi;
+                convert16(u[i], hide ? 0u : q8_factor_bf16x2(e), lo, hi);
+                if (big) {  // scales of 2 and above: some may need a second factor
+                    const uint32_t f2 = q8_excess_bf16x2(e);
+                    times4(lo, f2);
+                    times4(hi, f2);
                 }
+                const uint32_t dst = (at + i * 128) ^ (i << 4);  // (the swizzle's lower two bits)
+                st_smem_v4(dst, lo);
+                st_smem_v4(dst ^ 16, hi);
             }
-            if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, cur.kr);
+            if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, kr);
             __syncwarp();
             if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
-            ok = fetch(t + 1, cur);
+            ok = fetch(t + 1);
         }
     } else if (!kQ8 && (warp == kKWarp0 || warp == kVWarp0)) {
         // ------------------------------------------ bf16 operands reported (and cleaned)
@@ -786,6 +770,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 #pragma unroll 1
             for (int c = 128 * qd; c < 128 * qd + 128; c += 32) {
                 const int d = qd * 256 + hf * 128 + (c & 127);
+                const int swap = kQ8 ? (c & 64) >> 3 : 0;  // groups of eight dims are swapped in odd slices
                 uint32_t o[32];
                 if (nt > 0) {
                     tmem_ld32(tmem + lane_base + kColO + c, o);
@@ -800,9 +785,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                         f[i] = empty ? 0.f : __uint_as_float(o[j + n]) * inv;
                     }
                     if (bf)
-                        *reinterpret_cast<uint2*>(srow + 2 * (d + j)) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+                        *reinterpret_cast<uint2*>(srow + 2 * (d + (j ^ swap))) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
                     else
-                        *reinterpret_cast<float4*>(srow + 4 * (d + j)) = make_float4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<float4*>(srow + 4 * (d + (j ^ swap))) = make_float4(f[0], f[1], f[2], f[3]);
                 }
             }
             fence_proxy_async_smem();

@@ -80,7 +80,7 @@ static sa_status check_cache(const void* c_cache, sa_dtype cache_dtype, int64_t 
     if (c_ld % (cache_dtype == SA_E4M3 ? 16 : 8) != 0) return SA_EINVAL;
     if (c_scale && (scale_ld < d_c / 128 || scale_ld % 4 != 0 || !aligned(c_scale, 4))) return SA_EINVAL;
     if (!aligned(page_table, 4) || !aligned(seq_of_row, 4)) return SA_EINVAL;
-    if (pool_pages > kMaxPoolRows / 64) return SA_EUNSUPPORTED;
+    if (pool_pages > kMaxPoolRows / 64 || c_ld > INT32_MAX || kr_ld > INT32_MAX) return SA_EUNSUPPORTED;
     return SA_OK;
 }
 
