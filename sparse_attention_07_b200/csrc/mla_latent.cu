@@ -16,19 +16,13 @@
 //    score product's B operand (576 dims, K-major, two stages) and 256 dims of all
 //    64 as its half of the aggregation's (MN-major).  bf16 rows (of a prefix: whole
 //    pages) are TMA-loaded into the operands.  e4m3 rows are loaded to registers by
-//    eight warps, a tile ahead, turned into bf16 there, exactly, and stored to the
-//    operands, four warps each; one warp resolves their pool rows and scales, one
-//    reports stored operands.  Latent dims stand in the order 0, 2, 1, 3 of
-//    each four (fewer shifts), and in odd 64-dim slices with neighbouring groups of
-//    eight swapped (banks), in the query and the output columns alike.
-//    Measured and dropped for the e4m3 rows: cp.async into shared memory (its
-//    requests hold up the barrier arrivals between the CTAs: 2000 cycles per
-//    tile), four-row TMA gathers (200 cycles each beside the products, 16 per
-//    tile), and sending the rows that the partner aggregates through distributed
-//    shared memory (16 KB per tile at 20 bytes per clock from stores, 10 from bulk
-//    copies and st.async, and a cluster-scope release per tile).
-//  * Four softmax warps: thread = (row, half of the tile's keys).  Online base-2
-//    softmax; the two threads of a row exchange tile maxima through shared
+//    sixteen warps, whole lines, turned into bf16 there, exactly, and stored to the
+//    operands, eight warps each; one warp resolves their pool rows and scales, two
+//    report stored operands.  Latent dims stand in the order 0, 2, 1, 3 of each four
+//    (fewer shifts), and in odd 64-dim slices with neighbouring groups of eight
+//    swapped (banks), in the query and the output columns alike.
+//  * Eight softmax warps: thread = (row, quarter of the tile's keys).  Online base-2
+//    softmax; the four threads of a row exchange tile maxima through shared
 //    memory, O is rescaled only when a maximum grows by more than 2^8.  P goes
 //    to shared memory as bf16, as the tensor cores take it (half a step, 2^-8, of
 //    each weight); normaliser and lse use the fp32 values.
@@ -39,6 +33,16 @@
 //    row still get NaN, through its scores.
 //  * Few items split their keys over several pairs; partial states go to a
 //    workspace and a combine kernel merges them in split order.
+//
+// Measured: 1024 queries x 2048 selected e4m3 rows x 128 heads in 0.89 ms (655
+// TFLOP/s), 74 of them (one per pair) in 64 us: 1.56 us per tile and 14 us around
+// them.  The tensor cores are at work for 30 percent of that.  What is left is the
+// hand-over from role to role: with conversion, row loads and seven eighths of the
+// products left out a tile still takes 1.36 us.  So the warps are many (28, of 72
+// registers) and their loops short: fewer or longer ones ran slower (sixteen warps
+// of 128 registers 87 us; a second tile of rows in flight per warp, as copies or
+// as a doubled loop, 79 to 83; loading warps taking turns with double the rows 70),
+// softmax groups that alternate tiles and issuing products by readiness the same.
 #include "sa_device.cuh"
 #include "sa_internal.h"
 
@@ -55,7 +59,7 @@ constexpr int kSmxWarps = 8, kLoadWarps = 8;  // loading warps of either operand
 constexpr int kKWarp0 = kSmxWarps, kVWarp0 = kKWarp0 + kLoadWarps;
 constexpr int kMmaWarp = kVWarp0 + kLoadWarps;
 constexpr int kTmaWarp = kMmaWarp + 1;     // bf16: loads; e4m3: rows resolved
-constexpr int kReportWarp = kTmaWarp + 1;  // e4m3: stored operands reported, scores' and aggregation's
+constexpr int kReportWarp = kTmaWarp + 1;  // and the next: e4m3: stored operands reported, scores' and aggregation's
 constexpr int kThreads = 32 * (kReportWarp + 2);
 constexpr int kORow = 512 * 4 + 16;  // a staged output row (padded)
 
@@ -483,7 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         const int rr = 4 * lw + (lane >> 3);  // own row whose RoPE piece lane % 8 this lane moves (scores)
         const uint32_t rdst = smem_u32(sm + S::kOffR) + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4);
         uint64_t* freed = v ? bar_o : bar_s;
-        // The next tile's loads are under way during a tile's wait; a second tile ahead in registers gained nothing.
+        // The next tile's loads are under way while the warp waits for its stage.
         uint4 u[4], kr = make_uint4(0u, 0u, 0u, 0u);
         int4 row;  // pool rows (-1: none) and scale words of rows row0 .. row0 + 3
         uint4 sc;
@@ -817,14 +821,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-// Merge the split partial states: one warp per query row, lane owns dims
-// 4 lane + 128 p.
+// Merge the split partial states: one warp per query row and 128 of its dims,
+// four per lane; the loads of eight splits are under way together.
 constexpr int kCombThreads = 256;
 
 __global__ void __launch_bounds__(kCombThreads) mla_latent_combine_kernel(const Args ka) {
     pdl_wait();
     const LatentArgs& a = ka.a;
-    const int64_t orow = static_cast<int64_t>(blockIdx.x) * (kCombThreads / 32) + (threadIdx.x >> 5);
+    const int64_t orow = static_cast<int64_t>(blockIdx.x) * (kCombThreads / 128) + (threadIdx.x >> 7);
+    const int p = threadIdx.x >> 5 & 3;  // quarter of the dims
     if (orow >= static_cast<int64_t>(a.B) * a.T * a.H) return;
     const int lane = threadIdx.x & 31;
     const int h = static_cast<int>(orow % a.H), token = static_cast<int>(orow / a.H % a.T);
@@ -845,30 +850,29 @@ __global__ void __launch_bounds__(kCombThreads) mla_latent_combine_kernel(const 
     float L = ls * wgt;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    float4 acc[4];
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* src = reinterpret_cast<const float4*>(ka.ws_o + w0 * 512) + 32 * p + lane;
+    for (int s0 = 0; s0 < ka.nsplit; s0 += 8) {
+        float4 v[8];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) acc[p] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < ka.nsplit; ++s) {
-        const float w = __shfl_sync(0xffffffffu, wgt, s);
-        if (__shfl_sync(0xffffffffu, ls, s) == 0.f) continue;
-        const float4* src = reinterpret_cast<const float4*>(ka.ws_o + (w0 + static_cast<int64_t>(s) * 128) * 512) + lane;
+        for (int i = 0; i < 8; ++i) {
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s0 + i < ka.nsplit) v[i] = src[static_cast<int64_t>(s0 + i) * 128 * 128];
+        }
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const float4 v = src[32 * p];
-            acc[p].x += v.x * w, acc[p].y += v.y * w, acc[p].z += v.z * w, acc[p].w += v.w * w;
+        for (int i = 0; i < 8; ++i) {
+            const float w = __shfl_sync(0xffffffffu, wgt, s0 + i);  // (s0 + i < 32: weights past nsplit are 0)
+            acc.x += v[i].x * w, acc.y += v[i].y * w, acc.z += v[i].z * w, acc.w += v[i].w * w;
         }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const float x = acc[p].x * inv, y = acc[p].y * inv, z = acc[p].z * inv, w = acc[p].w * inv;
-        if (a.out_bf16)
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out_bf16) + orow * 1024 + 256 * p + 8 * lane) =
-                make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
-        else
-            *reinterpret_cast<float4*>(a.out + orow * 512 + 128 * p + 4 * lane) = make_float4(x, y, z, w);
-    }
-    if (a.lse && lane == 0) a.lse[orow] = L == 0.f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
+    const float x = acc.x * inv, y = acc.y * inv, z = acc.z * inv, w = acc.w * inv;
+    if (a.out_bf16)
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out_bf16) + orow * 1024 + 256 * p + 8 * lane) =
+            make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
+    else
+        *reinterpret_cast<float4*>(a.out + orow * 512 + 128 * p + 4 * lane) = make_float4(x, y, z, w);
+    if (a.lse && p == 0 && lane == 0) a.lse[orow] = L == 0.f ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
 }
 
 int tokens_per_item(int T, int H) {
@@ -933,7 +937,7 @@ sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cuda
     const sa_status s = a.c_scale ? launch<true>(ka, items, st) : launch<false>(ka, items, st);
     if (s == SA_OK && ka.nsplit > 1) {
         const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
-        constexpr int kPer = kCombThreads / 32;
+        constexpr int kPer = kCombThreads / 128;
         return launch_status(launch_pdl(mla_latent_combine_kernel, dim3(static_cast<unsigned>((rows + kPer - 1) / kPer)),
                                         dim3(kCombThreads), 0, st, ka));
     }
