@@ -458,14 +458,20 @@ def _need(t, name: str, dtypes, shape=None, contiguous=True):
     """Check one tensor argument: on the current device, of an allowed dtype,
     of the given shape (None: any extent) and, unless strides are passed on,
     contiguous."""
-    if t.get_device() != torch.cuda.current_device():
+    dev = t.get_device()  # (-1: not on a GPU)
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if shape is not None and t.shape != shape and (
-            t.dim() != len(shape) or any(w is not None and w != n for n, w in zip(t.shape, shape))):
-        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
-                         f"not {tuple(t.shape)}")
+    if shape is not None:
+        have = t.shape
+        if have != shape:
+            ok = len(have) == len(shape)
+            for w, n in zip(shape, have):
+                ok = ok and (w is None or w == n)
+            if not ok:
+                raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
+                                 f"not {tuple(have)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
@@ -473,6 +479,7 @@ def _need(t, name: str, dtypes, shape=None, contiguous=True):
 
 _SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
 _IO_TYPES = (torch.bfloat16, torch.float32)
+_F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
 
 
 def _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows):
@@ -484,7 +491,7 @@ def _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_ro
     if n == 0 or n % 64:
         raise ValueError(f"the cache holds whole pages of 64 rows, not {n} rows")
     _need(c_cache, "c_cache", (torch.float8_e4m3fn, torch.bfloat16), (n, 512), contiguous=False)
-    _need(kr_cache, "kr_cache", (torch.bfloat16,), (n, 64), contiguous=False)
+    _need(kr_cache, "kr_cache", _BF16, (n, 64), contiguous=False)
     (c_ld, one), (kr_ld, one_kr), s_ld = c_cache.stride(), kr_cache.stride(), 0
     if quantised:
         _need(c_scale, "c_scale", _SCALE_TYPES, (n, 4), contiguous=False)
@@ -493,30 +500,36 @@ def _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_ro
     if one != 1 or one_kr != 1:
         raise ValueError("the dims of a cache row must be contiguous")
     if page_table is not None:
-        _need(page_table, "page_table", (torch.int32,), (None, pages_per_seq))
+        _need(page_table, "page_table", _I32, (None, pages_per_seq))
     if seq_of_row is not None:
-        _need(seq_of_row, "seq_of_row", (torch.int32,), (rows,))
+        _need(seq_of_row, "seq_of_row", _I32, (rows,))
     elif page_table is not None and page_table.shape[0] < rows:
         raise ValueError(f"page_table has {page_table.shape[0]} sequences for {rows} rows")
     return SA_E4M3 if quantised else SA_BF16, c_ld, s_ld, kr_ld, n // 64
 
 
 def _need_tables(cos, sin, half):
-    _need(cos, "cos", (torch.float32,), (None, half))
-    _need(sin, "sin", (torch.float32,), tuple(cos.shape))
+    _need(cos, "cos", _F32, (None, half))
+    _need(sin, "sin", _F32, cos.shape)
 
 
 def _heads_out(x, out):
-    """Output of per-head rows x [tokens, H, D], made when not given."""
+    """(output of per-head rows x [tokens, H, D], made when not given, token
+    and head strides of x and of it)."""
+    tokens, H, D = x.shape
+    xt, xh, one = x.stride()
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ot, oh = H * D, D
     else:
-        _need(out, "output", (x.dtype,), x.shape, contiguous=False)
-        if (out.stride(0) == 0 and x.shape[0] > 1) or (out.stride(1) == 0 and x.shape[1] > 1):
+        _need(out, "output", (x.dtype,), (tokens, H, D), contiguous=False)
+        ot, oh, one_out = out.stride()
+        if (ot == 0 and tokens > 1) or (oh == 0 and H > 1):
             raise ValueError("an output must not be a broadcast view")
-    if x.shape[2] > 1 and (x.stride(2) != 1 or out.stride(2) != 1):
+        one *= one_out
+    if D > 1 and one != 1:
         raise ValueError("the dims of a head must be contiguous")
-    return out
+    return out, (x.data_ptr(), xt, xh, out.data_ptr(), ot, oh, H)
 
 
 def _code(t) -> int:
@@ -531,30 +544,31 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps: f
     by row positions[t] of cos and sin [n_pos, rope_dims/2] fp32, in split
     halves or interleaved pairs; cos = sin = None: no rotation.  Token and
     head strides are free; q_out and k_out may be q and k.  Returns (q_out, k_out)."""
-    tokens, Hq, D = q.shape
+    tokens, _, D = q.shape
     _need(q, "q", _IO_TYPES, contiguous=False)
-    q_out = _heads_out(q, q_out)
+    q_out, queries = _heads_out(q, q_out)
     keys = (None, 0, 0, None, 0, 0, 0)
     if k is not None:
         _need(k, "k", (q.dtype,), (tokens, None, D), contiguous=False)
-        k_out = _heads_out(k, k_out)
-        ks, os = k.stride(), k_out.stride()
-        keys = (k.data_ptr(), ks[0], ks[1], k_out.data_ptr(), os[0], os[1], k.shape[1])
+        k_out, keys = _heads_out(k, k_out)
     else:
         k_out = None
     if q_weight is not None:
-        _need(q_weight, "q_weight", (torch.float32,), (D,))
+        _need(q_weight, "q_weight", _F32, (D,))
     if k_weight is not None:
-        _need(k_weight, "k_weight", (torch.float32,), (D,))
-    rope = 0 if cos is None else 2 * cos.shape[1]
-    if rope:
-        _need_tables(cos, sin, rope // 2)
-        _need(positions, "positions", (torch.int32,), (tokens,))
-    qs, os = q.stride(), q_out.stride()
-    st = lib().sa_qk_norm_rope(q.data_ptr(), qs[0], qs[1], q_out.data_ptr(), os[0], os[1], Hq, *keys, _code(q),
-                               _p(q_weight), _p(k_weight), int(bool(norm)), float(eps), _p(cos), _p(sin),
-                               cos.shape[0] if rope else 0, _p(positions), tokens, D, rope_start, rope,
-                               int(bool(interleaved)), _stream())
+        _need(k_weight, "k_weight", _F32, (D,))
+    n_pos = half = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin come together")
+    if cos is not None:
+        n_pos, half = cos.shape
+    if half:
+        _need(cos, "cos", _F32)
+        _need(sin, "sin", _F32, (n_pos, half))
+        _need(positions, "positions", _I32, (tokens,))
+    st = lib().sa_qk_norm_rope(*queries, *keys, _code(q), _p(q_weight), _p(k_weight), 1 if norm else 0, eps, _p(cos),
+                               _p(sin), n_pos, _p(positions), tokens, D, rope_start, 2 * half, 1 if interleaved else 0,
+                               _stream())
     _check("sa_qk_norm_rope", st)
     return q_out, k_out
 
@@ -573,11 +587,11 @@ def mla_cache_write(c, kr, c_cache, kr_cache, slots, pages_per_seq: int, cos, si
     _need(kr, "kr", (c.dtype,), (tokens, 64), contiguous=False)
     if c.stride(1) != 1 or kr.stride(1) != 1:
         raise ValueError("the dims of a token must be contiguous")
-    _need(slots, "slots", (torch.int32,), (tokens,))
+    _need(slots, "slots", _I32, (tokens,))
     if positions is not None:
-        _need(positions, "positions", (torch.int32,), (tokens,))
+        _need(positions, "positions", _I32, (tokens,))
     if weight is not None:
-        _need(weight, "weight", (torch.float32,), (512,))
+        _need(weight, "weight", _F32, (512,))
     _need_tables(cos, sin, 32)
     dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, tokens)
     st = lib().sa_mla_cache_write(_p(c), max(c.stride(0), 512), _p(kr), max(kr.stride(0), 64), _code(c), _p(weight),
@@ -593,16 +607,16 @@ def mla_cache_read(c_cache, kr_cache, idx, pages_per_seq: int, c_scale=None, pag
     """Rows of the latent cache at positions idx [rows, k] int32 (-1: zeros) of
     sequence seq_of_row[r], as bf16: (c [rows, k, 512], kr [rows, k, 64])."""
     rows, k = idx.shape
-    _need(idx, "idx", (torch.int32,))
+    _need(idx, "idx", _I32)
     dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
     if c_out is None:
         c_out = torch.empty(rows, k, 512, dtype=torch.bfloat16, device=idx.device)
     else:
-        _need(c_out, "c_out", (torch.bfloat16,), (rows, k, 512))
+        _need(c_out, "c_out", _BF16, (rows, k, 512))
     if kr_out is None:
         kr_out = torch.empty(rows, k, 64, dtype=torch.bfloat16, device=idx.device)
     else:
-        _need(kr_out, "kr_out", (torch.bfloat16,), (rows, k, 64))
+        _need(kr_out, "kr_out", _BF16, (rows, k, 64))
     st = lib().sa_mla_cache_read(_p(c_cache), dt, c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld, pool, _p(page_table),
                                  pages_per_seq, _p(seq_of_row), _p(idx), rows, k, 512, 64, _p(c_out), _p(kr_out),
                                  _stream())
@@ -625,14 +639,14 @@ def tree_mla_workspace_size(B: int, T: int, H: int, L_max: int) -> int:
 def _latent_io(q_lat, q_rope, out, lse, workspace, need: int):
     """Check queries [..., H, 512] / [..., H, 64]; make the output and the workspace when not given."""
     lead = tuple(q_lat.shape[:-1])
-    _need(q_lat, "q_lat", (torch.bfloat16,), lead + (512,))
-    _need(q_rope, "q_rope", (torch.bfloat16,), lead + (64,))
+    _need(q_lat, "q_lat", _BF16, lead + (512,))
+    _need(q_rope, "q_rope", _BF16, lead + (64,))
     if out is None:
         out = torch.empty(lead + (512,), dtype=torch.float32, device=q_lat.device)
     else:
         _need(out, "out", _IO_TYPES, lead + (512,))
     if lse is not None:
-        _need(lse, "lse", (torch.float32,), lead)
+        _need(lse, "lse", _F32, lead)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q_lat.device)
     if workspace is not None:
@@ -643,7 +657,7 @@ def _latent_io(q_lat, q_rope, out, lse, workspace, need: int):
 def _sparse_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, idx, scale, pages_per_seq, page_table, seq_of_row, out,
                    lse, workspace):
     rows, H, _ = q_lat.shape
-    _need(idx, "idx", (torch.int32,), (rows, None))
+    _need(idx, "idx", _I32, (rows, None))
     k = idx.shape[1]
     out, workspace, wbytes = _latent_io(q_lat, q_rope, out, lse, workspace, sparse_mla_q8_workspace_size(rows, H, k))
     _, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
@@ -657,7 +671,7 @@ def _sparse_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, idx, scale, pages_
 def _dense_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, n_visible, L_max, scale, pages_per_seq, page_table,
                   seq_of_row, out, lse, workspace):
     rows, H, _ = q_lat.shape
-    _need(n_visible, "n_visible", (torch.int32,), (rows,))
+    _need(n_visible, "n_visible", _I32, (rows,))
     out, workspace, wbytes = _latent_io(q_lat, q_rope, out, lse, workspace, dense_mla_q8_workspace_size(rows, H, L_max))
     _, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
     st = lib().sa_dense_mla_q8(_p(q_lat), _p(q_rope), _p(c_cache), c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld, pool,
@@ -676,9 +690,9 @@ def tree_mla_decode(q_lat, q_rope, c_cache, kr_cache, n_past, tree_mask, L_max: 
     cache is bf16, or e4m3 with `c_scale`.  [B, T, H, 512] fp32 (or bf16 when
     `out` is a bf16 tensor); rows i >= n_draft[b] are left as they were."""
     B, T, H, _ = q_lat.shape
-    _need(n_past, "n_past", (torch.int32,), (B,))
+    _need(n_past, "n_past", _I32, (B,))
     if n_draft is not None:
-        _need(n_draft, "n_draft", (torch.int32,), (B,))
+        _need(n_draft, "n_draft", _I32, (B,))
     if tree_mask is not None:
         _need(tree_mask, "tree_mask", (torch.uint8, torch.bool), (B, T, T))
     out, workspace, wbytes = _latent_io(q_lat, q_rope, out, lse, workspace, tree_mla_workspace_size(B, T, H, L_max))
