@@ -506,8 +506,9 @@ sa_status sa_topk_from_candidates(const uint64_t* cand, int64_t cand_ld, int32_t
  *   that side is left out (its pointers may be NULL).  weights [D] fp32 or NULL.
  *   rope_dims = 0: no rotation (tables and positions may be NULL).
  * D <= 512.  A position outside [0, n_pos) records code 0x900 in the device
- * error word and reads row 0.  Any element alignment is accepted; 16-byte
- * aligned pointers and strides with D a multiple of 8 up to 256 run faster.
+ * error word and reads row 0.  Any element alignment is accepted; pointers and
+ * strides aligned to four elements (weights and tables to 16 bytes), D and
+ * rope_dims multiples of 8, rope_start one of 4 and D <= 256 run faster.
  */
 sa_status sa_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_stride, void* q_out,
                           int64_t q_out_token_stride, int64_t q_out_head_stride, int H_q, const void* k,
@@ -537,7 +538,7 @@ sa_status sa_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_
  * the page table, or on a page outside the pool, is not written and records code
  * 0x700; a position outside the tables records 0x900 and reads row 0.  Alignment:
  * c, weight, c_cache, kr_cache and the c and cache row strides 16 bytes, c_scale
- * and scale_ld 4 bytes.  d_c = 512, d_R = 64.
+ * and scale_ld 4 bytes; cache row strides below 2^31.  d_c = 512, d_R = 64.
  */
 sa_status sa_mla_cache_write(const void* c, int64_t c_in_ld, const void* kr, int64_t kr_in_ld, sa_dtype in_dtype,
                              const float* weight, int norm, float eps, const float* cos, const float* sin,

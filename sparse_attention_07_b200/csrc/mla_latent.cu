@@ -148,7 +148,8 @@ __device__ __forceinline__ Item item_of(const Args& ka, int item) {
     it.i0 = (item % ka.groups) * ka.tokens_per_item;
     it.seq = a.seq_of_row ? a.seq_of_row[it.b] : it.b;
     it.nd = a.tree ? max(min(a.n_draft ? a.n_draft[it.b] : a.T, a.T), 0) : 0;
-    it.past = a.idx ? 0 : max(a.n_past[it.b], 0);
+    // (no further than the page table: what lies behind is recorded where it is resolved, for 64 positions)
+    it.past = a.idx ? 0 : static_cast<int>(min(static_cast<int64_t>(max(a.n_past[it.b], 0)), a.pages_per_seq * int64_t(kPage) + kPage));
     it.n_keys = a.idx ? a.k : it.past + it.nd;
     it.tokens = min(ka.tokens_per_item, (a.tree ? it.nd : a.T) - it.i0);  // <= 0: nothing to do
     return it;
@@ -516,8 +517,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         for (int t = 0; ok && t < nt; ++t) {
             const int tf = t - 2;  // the tile whose products free the stage
             if (tf >= 0 && !wait(&freed[tf & 1], static_cast<uint32_t>(tf >> 1 & 1), 8)) break;
-            // a drafted row's non-finite block (byte 255) stays out of the aggregation: its finite codes times 0
-            const int drafted_from = v && a.tree ? it.past - (t0 + t) * kNK - row0 : kNK;
             const uint32_t at = dst0 + (t & 1) * stage;
             const bool big = __any_sync(0xffffffffu, ((sc.x | sc.y | sc.z | sc.w) & 0x80808080u) != 0);
             const int rows[4] = {row.x, row.y, row.z, row.w};
@@ -525,9 +524,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t e = scs[i] >> sc_shift & 255u;
-                const bool hide = rows[i] < 0 || (e == 255u && i >= drafted_from);
                 uint4 lo, hi;
-                convert16(u[i], hide ? 0u : q8_factor_bf16x2(e), lo, hi);
+                convert16(u[i], rows[i] < 0 ? 0u : q8_factor_bf16x2(e), lo, hi);
                 if (big) {  // scales of 2 and above: some may need a second factor
                     const uint32_t f2 = q8_excess_bf16x2(e);
                     times4(lo, f2);
@@ -538,6 +536,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 st_smem_v4(dst ^ 16, hi);
             }
             if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, kr);
+            // drafted rows' non-finite pieces stay out of the aggregation
+            if (v && a.tree && (t0 + t + 1) * kNK > it.past) {
+#pragma unroll 1
+                for (int i = max(0, it.past - (t0 + t) * kNK - row0); i < 4; ++i) {
+                    const uint32_t dst = (at + i * 128) ^ (i << 4);
+                    if (bad4(ld_smem_v4(dst))) st_smem_v4(dst, make_uint4(0u, 0u, 0u, 0u));
+                    if (bad4(ld_smem_v4(dst ^ 16))) st_smem_v4(dst ^ 16, make_uint4(0u, 0u, 0u, 0u));
+                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
             ok = fetch(t + 1);
