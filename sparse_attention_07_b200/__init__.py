@@ -233,7 +233,13 @@ def sparse_mla_workspace_size(rows: int, H: int, k: int, d_c: int = 512) -> int:
     return int(lib().sa_sparse_mla_workspace_size(rows, H, k, d_c))
 
 
+def _plain_cache(c_cache):
+    if c_cache.dtype == torch.float8_e4m3fn:
+        raise ValueError("an e4m3 cache needs c_scale")
+
+
 def _mla_args(q_lat, q_rope, c_cache, kr_cache, idx, out, lse):
+    _plain_cache(c_cache)
     rows, H, d_c = q_lat.shape
     d_R = q_rope.shape[2]
     k = idx.shape[1]
@@ -304,6 +310,7 @@ def dense_mla_decode(q_lat, q_rope, c_cache, kr_cache, n_visible, L_max: int, sc
     if c_scale is not None:
         return _dense_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, n_visible, L_max, scale, pages_per_seq,
                              page_table, seq_of_row, out, lse, workspace)
+    _plain_cache(c_cache)
     rows, H, d_c = q_lat.shape
     d_R = q_rope.shape[2]
     if out is None:
@@ -594,7 +601,8 @@ def mla_cache_write(c, kr, c_cache, kr_cache, slots, pages_per_seq: int, cos, si
         _need(weight, "weight", _F32, (512,))
     _need_tables(cos, sin, 32)
     dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, tokens)
-    st = lib().sa_mla_cache_write(_p(c), max(c.stride(0), 512), _p(kr), max(kr.stride(0), 64), _code(c), _p(weight),
+    c_in_ld, kr_in_ld = (c.stride(0), kr.stride(0)) if tokens > 1 else (512, 64)
+    st = lib().sa_mla_cache_write(_p(c), c_in_ld, _p(kr), kr_in_ld, _code(c), _p(weight),
                                   int(bool(norm)), float(eps), _p(cos), _p(sin), cos.shape[0], _p(positions),
                                   int(bool(interleaved)), _p(c_cache), dt, c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld,
                                   pool, _p(page_table), pages_per_seq, _p(seq_of_row), _p(slots), tokens, 512, 64,

@@ -10,6 +10,7 @@ namespace {
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 constexpr int64_t kMaxPoolRows = int64_t(1) << 31;
+constexpr int kMaxKeys = 1 << 30;  // of one row: tiles of them are counted in 32 bits
 
 }  // namespace
 
@@ -175,7 +176,7 @@ static sa_status latent_attn(const void* q_lat, const void* q_rope, const void* 
     const sa_status s = check_cache(c_cache, cache_dtype, c_ld, c_scale, scale_ld, kr_cache, kr_ld, pool_pages,
                                     page_table, pages_per_seq, seq_of_row, d_c, d_R);
     if (s != SA_OK) return s;
-    if (H > 128 || T > SA_TREE_MAX_TOKENS || (out_dtype != SA_F32 && out_dtype != SA_BF16)) return SA_EUNSUPPORTED;
+    if (H > 128 || T > SA_TREE_MAX_TOKENS || k > kMaxKeys || (out_dtype != SA_F32 && out_dtype != SA_BF16)) return SA_EUNSUPPORTED;
     if (!q_lat || !q_rope || !out || (!idx && !n_past)) return SA_EINVAL;
     if (!aligned(q_lat, 16) || !aligned(q_rope, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(idx, 4) ||
         !aligned(n_past, 4) || !aligned(n_draft, 4))
@@ -214,7 +215,7 @@ static sa_status latent_attn(const void* q_lat, const void* q_rope, const void* 
 }
 
 size_t sa_sparse_mla_q8_workspace_size(int rows, int H, int k) {
-    if (rows < 1 || H < 1 || k < 1) return 0;
+    if (rows < 1 || H < 1 || k < 1 || k > kMaxKeys) return 0;
     return mla_latent_workspace_bytes(rows, 1, H, k);
 }
 
@@ -244,7 +245,7 @@ sa_status sa_dense_mla_q8(const void* q_lat, const void* q_rope, const void* c_c
 }
 
 size_t sa_tree_mla_workspace_size(int B, int T, int H, int L_max) {
-    if (B < 1 || T < 1 || H < 1 || L_max < 1) return 0;
+    if (B < 1 || T < 1 || H < 1 || L_max < 1 || L_max > kMaxKeys) return 0;
     return mla_latent_workspace_bytes(B, T, H, L_max);
 }
 

@@ -102,6 +102,31 @@ def test_workspace_sizes(L):
         assert L.sa_sparse_mla_q8(*a, FAKE, need - 1, None) == sa.SA_EINVAL
 
 
+def test_more_keys_than_32_bits_of_tiles_hold(L):
+    assert L.sa_sparse_mla_q8_workspace_size(1, 128, 2 ** 31 - 1) == 0
+    assert L.sa_tree_mla_workspace_size(1, 1, 128, 2 ** 31 - 1) == 0
+    call = caller(L.sa_sparse_mla_q8, ql=FAKE, qr=FAKE, cc=FAKE, cld=512, cs=FAKE, sld=4, krc=FAKE, krld=64, pool=4,
+                  pt=None, pps=4, sor=None, idx=FAKE, rows=1, H=128, k=2 ** 30 + 1, dc=512, dR=64, scale=0.07, out=FAKE,
+                  odt=sa.SA_F32, lse=None, ws=None, wsb=0, st=None)
+    assert call() == sa.SA_EUNSUPPORTED
+    assert call(k=64, cld=2 ** 31) == sa.SA_EUNSUPPORTED
+    assert call(k=64, krld=2 ** 31) == sa.SA_EUNSUPPORTED
+
+
+def test_a_quantised_cache_without_its_scales_is_refused():
+    """Without c_scale the calls read a bf16 cache, twice an e4m3 one's bytes."""
+    q, qr = torch.zeros(1, 2, 512).bfloat16(), torch.zeros(1, 2, 64).bfloat16()
+    c, kr = torch.zeros(64, 512).to(torch.float8_e4m3fn), torch.zeros(64, 64).bfloat16()
+    one = torch.zeros(1, 1, dtype=torch.int32)
+    for call in (sa.sparse_mla_decode, sa.sparse_mla_prefill):
+        with pytest.raises(ValueError):
+            call(q, qr, c, kr, one, 0.07, 1)
+    with pytest.raises(ValueError):
+        sa.sparse_mla_decode_static(q, qr, c, kr, one, 0.07, 1)
+    with pytest.raises(ValueError):
+        sa.dense_mla_decode(q, qr, c, kr, one[0], 1, 0.07, 1)
+
+
 def test_cpu_tensors_are_refused():
     q = torch.zeros(1, 2, 64)
     with pytest.raises(ValueError):

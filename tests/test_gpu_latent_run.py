@@ -256,6 +256,17 @@ def test_an_overflowing_drafted_row_stays_with_its_tokens():
         check_attention(out[0, i], None, attend64(q[0, i], qr[0, i], cache, 0, pos), f"token {i}")
 
 
+def test_broadcast_token_rows_are_refused():
+    """Rows of the written tokens that overlap (stride 0) are not a layout the write reads."""
+    cache = make_cache((64, 64), True, 2, DEV)
+    cos, sin = tables(8, D_R, DEV)
+    c, kr = torch.zeros(1, D_C, device=DEV).bfloat16(), torch.zeros(1, D_R, device=DEV).bfloat16()
+    for a, b in ((c.expand(2, D_C), kr.repeat(2, 1)), (c.repeat(2, 1), kr.expand(2, D_R))):
+        with pytest.raises(sa.SparseAttnError):
+            sa.mla_cache_write(a, b, cache["c_cache"], cache["kr_cache"], ints([0, 0]), cache["pps"], cos, sin,
+                               c_scale=cache["c_scale"], page_table=cache["page_table"])
+
+
 @pytest.mark.parametrize("q8", [True, False])
 def test_a_length_past_the_page_table_is_reported(q8):
     """A length no page table holds is recorded and costs no more than the table's own positions."""
