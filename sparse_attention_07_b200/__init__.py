@@ -463,28 +463,22 @@ def csa_window_index(topk_idx, raw_len, window: int, win_base: int, idx_out=None
 
 def _need(t, name: str, dtypes, shape=None, contiguous=True):
     """Check one tensor argument: on the current device, of an allowed dtype,
-    of the given shape (None: any extent) and, unless strides are passed on,
-    contiguous."""
+    of the given shape and, unless strides are passed on, contiguous."""
     dev = t.get_device()  # (-1: not on a GPU)
+    if dev >= 0 and dev == torch._C._cuda_getDevice() and t.dtype in dtypes and (
+            shape is None or t.shape == shape) and (not contiguous or t.is_contiguous()):
+        return
     if dev < 0 or dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name} must be on the current CUDA device, not on {t.device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {t.dtype}")
-    if shape is not None:
-        have = t.shape
-        if have != shape:
-            ok = len(have) == len(shape)
-            for w, n in zip(shape, have):
-                ok = ok and (w is None or w == n)
-            if not ok:
-                raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, "
-                                 f"not {tuple(have)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 _SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+_POOL_TYPES = (torch.float8_e4m3fn, torch.bfloat16)
 _IO_TYPES = (torch.bfloat16, torch.float32)
 _F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
 
@@ -497,27 +491,31 @@ def _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_ro
         raise ValueError("an e4m3 cache needs c_scale, a bf16 cache has none")
     if n == 0 or n % 64:
         raise ValueError(f"the cache holds whole pages of 64 rows, not {n} rows")
-    _need(c_cache, "c_cache", (torch.float8_e4m3fn, torch.bfloat16), (n, 512), contiguous=False)
-    _need(kr_cache, "kr_cache", _BF16, (n, 64), contiguous=False)
+    _need(c_cache, "c_cache", _POOL_TYPES, (n, 512), False)
+    _need(kr_cache, "kr_cache", _BF16, (n, 64), False)
     (c_ld, one), (kr_ld, one_kr), s_ld = c_cache.stride(), kr_cache.stride(), 0
     if quantised:
-        _need(c_scale, "c_scale", _SCALE_TYPES, (n, 4), contiguous=False)
+        _need(c_scale, "c_scale", _SCALE_TYPES, (n, 4), False)
         s_ld, one_s = c_scale.stride()
         one *= one_s
     if one != 1 or one_kr != 1:
         raise ValueError("the dims of a cache row must be contiguous")
-    if page_table is not None:
-        _need(page_table, "page_table", _I32, (None, pages_per_seq))
     if seq_of_row is not None:
         _need(seq_of_row, "seq_of_row", _I32, (rows,))
-    elif page_table is not None and page_table.shape[0] < rows:
-        raise ValueError(f"page_table has {page_table.shape[0]} sequences for {rows} rows")
+    if page_table is not None:
+        seqs = page_table.shape[0]
+        _need(page_table, "page_table", _I32, (seqs, pages_per_seq))
+        if seq_of_row is None and seqs < rows:
+            raise ValueError(f"page_table has {seqs} sequences for {rows} rows")
     return SA_E4M3 if quantised else SA_BF16, c_ld, s_ld, kr_ld, n // 64
 
 
-def _need_tables(cos, sin, half):
-    _need(cos, "cos", _F32, (None, half))
-    _need(sin, "sin", _F32, cos.shape)
+def _need_tables(cos, sin, half) -> int:
+    """Check the tables of `half` pairs; return their number of positions."""
+    shape = (cos.shape[0], half)
+    _need(cos, "cos", _F32, shape)
+    _need(sin, "sin", _F32, shape)
+    return shape[0]
 
 
 def _heads_out(x, out):
@@ -552,11 +550,11 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps: f
     halves or interleaved pairs; cos = sin = None: no rotation.  Token and
     head strides are free; q_out and k_out may be q and k.  Returns (q_out, k_out)."""
     tokens, _, D = q.shape
-    _need(q, "q", _IO_TYPES, contiguous=False)
+    _need(q, "q", _IO_TYPES, None, False)
     q_out, queries = _heads_out(q, q_out)
     keys = (None, 0, 0, None, 0, 0, 0)
     if k is not None:
-        _need(k, "k", (q.dtype,), (tokens, None, D), contiguous=False)
+        _need(k, "k", (q.dtype,), (tokens, k.shape[1], D), False)
         k_out, keys = _heads_out(k, k_out)
     else:
         k_out = None
@@ -567,11 +565,9 @@ def qk_norm_rope(q, k, cos, sin, positions, q_weight=None, k_weight=None, eps: f
     n_pos = half = 0
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin come together")
-    if cos is not None:
-        n_pos, half = cos.shape
-    if half:
-        _need(cos, "cos", _F32)
-        _need(sin, "sin", _F32, (n_pos, half))
+    if cos is not None and cos.shape[1]:
+        half = cos.shape[1]
+        n_pos = _need_tables(cos, sin, half)
         _need(positions, "positions", _I32, (tokens,))
     st = lib().sa_qk_norm_rope(*queries, *keys, _code(q), _p(q_weight), _p(k_weight), 1 if norm else 0, eps, _p(cos),
                                _p(sin), n_pos, _p(positions), tokens, D, rope_start, 2 * half, 1 if interleaved else 0,
@@ -590,8 +586,8 @@ def mla_cache_write(c, kr, c_cache, kr_cache, slots, pages_per_seq: int, cos, si
     cos and sin [n_pos, 32].  slots [tokens] int32: position of the token in
     sequence seq_of_row[t] (None: t), -1: skip the token."""
     tokens = c.shape[0]
-    _need(c, "c", _IO_TYPES, (tokens, 512), contiguous=False)
-    _need(kr, "kr", (c.dtype,), (tokens, 64), contiguous=False)
+    _need(c, "c", _IO_TYPES, (tokens, 512), False)
+    _need(kr, "kr", (c.dtype,), (tokens, 64), False)
     if c.stride(1) != 1 or kr.stride(1) != 1:
         raise ValueError("the dims of a token must be contiguous")
     _need(slots, "slots", _I32, (tokens,))
@@ -599,11 +595,11 @@ def mla_cache_write(c, kr, c_cache, kr_cache, slots, pages_per_seq: int, cos, si
         _need(positions, "positions", _I32, (tokens,))
     if weight is not None:
         _need(weight, "weight", _F32, (512,))
-    _need_tables(cos, sin, 32)
+    n_pos = _need_tables(cos, sin, 32)
     dt, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, tokens)
     c_in_ld, kr_in_ld = (c.stride(0), kr.stride(0)) if tokens > 1 else (512, 64)
     st = lib().sa_mla_cache_write(_p(c), c_in_ld, _p(kr), kr_in_ld, _code(c), _p(weight),
-                                  int(bool(norm)), float(eps), _p(cos), _p(sin), cos.shape[0], _p(positions),
+                                  1 if norm else 0, eps, _p(cos), _p(sin), n_pos, _p(positions),
                                   int(bool(interleaved)), _p(c_cache), dt, c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld,
                                   pool, _p(page_table), pages_per_seq, _p(seq_of_row), _p(slots), tokens, 512, 64,
                                   _stream())
@@ -665,8 +661,8 @@ def _latent_io(q_lat, q_rope, out, lse, workspace, need: int):
 def _sparse_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, idx, scale, pages_per_seq, page_table, seq_of_row, out,
                    lse, workspace):
     rows, H, _ = q_lat.shape
-    _need(idx, "idx", _I32, (rows, None))
     k = idx.shape[1]
+    _need(idx, "idx", _I32, (rows, k))
     out, workspace, wbytes = _latent_io(q_lat, q_rope, out, lse, workspace, sparse_mla_q8_workspace_size(rows, H, k))
     _, c_ld, s_ld, kr_ld, pool = _need_cache(c_cache, c_scale, kr_cache, pages_per_seq, page_table, seq_of_row, rows)
     st = lib().sa_sparse_mla_q8(_p(q_lat), _p(q_rope), _p(c_cache), c_ld, _p(c_scale), s_ld, _p(kr_cache), kr_ld, pool,
