@@ -33,9 +33,13 @@
 //    row still get NaN, through its scores.
 //  * Few items split their keys over several pairs; partial states go to a
 //    workspace and a combine kernel merges them in split order.
+//  * Many short selections go to the pairs in turn (kMany): the tiles of a pair's items
+//    are one stream for the roles, the loading warps bring the next query when an
+//    item's scores are done, and its output leaves straight from tensor memory while
+//    the next item's tiles are under way.
 //
-// Measured: 1024 queries x 2048 selected e4m3 rows x 128 heads in 0.89 ms (655
-// TFLOP/s), 74 of them (one per pair) in 64 us: 1.56 us per tile and 14 us around
+// Measured: 1024 queries x 2048 selected e4m3 rows x 128 heads in 0.87 ms (669
+// TFLOP/s), 74 of them (one per pair) in 63 us: 1.55 us per tile and 14 us around
 // them.  The tensor cores are at work for 30 percent of that.  What is left is the
 // hand-over from role to role: with conversion, row loads and seven eighths of the
 // products left out a tile still takes 1.36 us.  So the warps are many (28, of 72
@@ -43,6 +47,8 @@
 // of 128 registers 87 us; a second tile of rows in flight per warp, as copies or
 // as a doubled loop, 79 to 83; loading warps taking turns with double the rows 70),
 // softmax groups that alternate tiles and issuing products by readiness the same.
+#include <algorithm>
+
 #include "sa_device.cuh"
 #include "sa_internal.h"
 
@@ -55,13 +61,13 @@ constexpr int kOwn = 32;   // keys of a tile that one CTA loads
 constexpr int kRows = 64;  // query rows per CTA
 constexpr int kQSlice = kRows * 128, kKSlice = kOwn * 128, kVSlice = kNK * 128;  // 64 dims each
 constexpr int kVStage = 4 * kVSlice;
+constexpr int kORow = 512 * 4 + 16;  // a staged output row (padded)
 constexpr int kSmxWarps = 8, kLoadWarps = 8;  // loading warps of either operand
 constexpr int kKWarp0 = kSmxWarps, kVWarp0 = kKWarp0 + kLoadWarps;
 constexpr int kMmaWarp = kVWarp0 + kLoadWarps;
 constexpr int kTmaWarp = kMmaWarp + 1;     // bf16: loads; e4m3: rows resolved
 constexpr int kReportWarp = kTmaWarp + 1;  // and the next: e4m3: stored operands reported, scores' and aggregation's
 constexpr int kThreads = 32 * (kReportWarp + 2);
-constexpr int kORow = 512 * 4 + 16;  // a staged output row (padded)
 
 template <bool kQ8>
 struct Smem {
@@ -72,9 +78,9 @@ struct Smem {
     static constexpr int kOffP = kOffV + 2 * kVStage;
     static constexpr int kEnd = kOffP + kRows * 128;
     static constexpr int kBytes = kEnd + 1024;
+    static_assert(kRows * kORow <= kEnd, "the output rows fit");
     static_assert(kOffK % 1024 == 0 && kOffR % 1024 == 0 && kOffV % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms are 1024-byte aligned");
     static_assert(kBytes <= 232448 - 4096, "shared memory budget");
-    static_assert(kRows * kORow <= kEnd, "the output rows fit");
 };
 
 // Tiles whose rows are resolved ahead: the warps of the score operand run up to three
@@ -97,6 +103,7 @@ struct Args {
     int tokens_per_item;  // P: tokens of a tree in one item's 128 rows
     int groups;           // items per tree
     int nsplit;
+    int items, stride;  // stride > 0 (selections): a pair takes items p, p + stride, ... of them, of equal tiles
     float* ws_o;   // [item][nsplit][128][512]
     float* ws_ml;  // [item][nsplit][128][2]: m, l
 };
@@ -127,6 +134,14 @@ struct Waits {
         }
         return true;
     }
+    // (one lane) Without the abort word: for a role's own work in flight.
+    __device__ __forceinline__ static bool own(uint64_t* b, uint32_t parity, uint32_t limit_ns) {
+        const uint32_t t0 = now();
+#pragma unroll 1
+        while (!mbar_try_wait(b, parity))
+            if (now() - t0 > limit_ns) return false;
+        return true;
+    }
     // The whole warp leaves together.
     __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity, int site) const {
         if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
@@ -155,16 +170,12 @@ __device__ __forceinline__ Item item_of(const Args& ka, int item) {
     return it;
 }
 
-// Pool row of a slot of an item's keys in three steps, each one load that has
+// Pool row of a slot of a row's keys in three steps, each one load that has
 // a while to land: the slot's position (-1: none), the page that holds it, the
 // row.  A broken page table is recorded and row 0 of the pool read instead.
-__device__ __forceinline__ int key_position(const LatentArgs& a, const Item& it, bool in, int slot) {
-    if (!in || slot >= it.n_keys) return -1;
-    return a.idx ? a.idx[static_cast<int64_t>(it.b) * a.k + slot] : slot;
-}
-__device__ __forceinline__ int key_page(const LatentArgs& a, const Item& it, int pos) {
+__device__ __forceinline__ int key_page(const LatentArgs& a, int seq, int pos) {
     if (pos < 0 || pos / kPage >= a.pages_per_seq) return -1;
-    const int64_t at = static_cast<int64_t>(it.seq) * a.pages_per_seq + pos / kPage;
+    const int64_t at = static_cast<int64_t>(seq) * a.pages_per_seq + pos / kPage;
     return a.page_table ? a.page_table[at] : (at < a.pool_pages ? static_cast<int>(at) : -1);
 }
 __device__ __forceinline__ int key_row(const LatentArgs& a, int pos, int page, bool& broken) {
@@ -173,39 +184,58 @@ __device__ __forceinline__ int key_row(const LatentArgs& a, int pos, int page, b
     return pos < 0 ? -1 : ok ? page * kPage + (pos % kPage) : 0;
 }
 
-// Pool rows and scale words of 32 keys (lane = key) of the tiles to come: the next
-// tile's are known, the one after has its page under way, the third its position.
-template <bool kQ8>
+// Pool rows and scale words of 32 keys (lane = key) of the tiles to come, of one item
+// after the other: the next tile's are known, the one after has its page under way, the
+// third its position.
+template <bool kQ8, bool kMany>
 struct Rows {
-    int row, next, pos2, page2, pos3;
+    int row, next, pos2, page2, pos3, seq3;
     uint32_t sc, sc_next;
+    int b, seq, t;  // the tile whose position comes next
     bool broken;
 
     __device__ __forceinline__ uint32_t scale_word(const LatentArgs& a, int r) const {
         return kQ8 && r >= 0 ? __ldg(reinterpret_cast<const uint32_t*>(a.c_scale + r * a.s_ld)) : 0x7F7F7F7Fu;
     }
-    // slot: the lane's key of tile 0
-    __device__ __forceinline__ void start(const LatentArgs& a, const Item& it, int nt, int slot) {
-        const int p0 = key_position(a, it, 0 < nt, slot), p1 = key_position(a, it, 1 < nt, slot + kNK);
-        pos2 = key_position(a, it, 2 < nt, slot + 2 * kNK);
-        pos3 = key_position(a, it, 3 < nt, slot + 3 * kNK);
-        const int g0 = key_page(a, it, p0), g1 = key_page(a, it, p1);
-        page2 = key_page(a, it, pos2);
+    // slot: the lane's key of an item's tile 0
+    __device__ __forceinline__ int position(const Args& ka, const Item& it, int nt, int slot) {
+        const LatentArgs& a = ka.a;
+        if (kMany && t == nt) {
+            t = 0;
+            b += ka.stride;
+            if (b < ka.items) seq = a.seq_of_row ? a.seq_of_row[b] : b;
+        }
+        const int at = slot + t * kNK;
+        int pos = -1;
+        if ((kMany ? b < ka.items : t < nt) && at < it.n_keys) pos = a.idx ? a.idx[static_cast<int64_t>(b) * a.k + at] : at;
+        seq3 = seq;
+        ++t;
+        return pos;
+    }
+    __device__ __forceinline__ void start(const Args& ka, const Item& it, int nt, int slot) {
+        const LatentArgs& a = ka.a;
+        b = it.b, seq = it.seq, t = 0;
+        const int p0 = position(ka, it, nt, slot), s0 = seq3, p1 = position(ka, it, nt, slot), s1 = seq3;
+        pos2 = position(ka, it, nt, slot);
+        const int s2 = seq3;
+        pos3 = position(ka, it, nt, slot);
+        const int g0 = key_page(a, s0, p0), g1 = key_page(a, s1, p1);
+        page2 = key_page(a, s2, pos2);
         broken = false;
         row = key_row(a, p0, g0, broken);
         next = key_row(a, p1, g1, broken);
         sc = scale_word(a, row);
         sc_next = scale_word(a, next);
     }
-    // t: the new current tile
-    __device__ __forceinline__ void advance(const LatentArgs& a, const Item& it, int nt, int slot, int t) {
+    __device__ __forceinline__ void advance(const Args& ka, const Item& it, int nt, int slot) {
+        const LatentArgs& a = ka.a;
         row = next;
         sc = sc_next;
         next = key_row(a, pos2, page2, broken);
         sc_next = scale_word(a, next);
         pos2 = pos3;
-        page2 = key_page(a, it, pos2);
-        pos3 = key_position(a, it, t + 3 < nt, slot + (t + 3) * kNK);
+        page2 = key_page(a, seq3, pos2);
+        pos3 = position(ka, it, nt, slot);
     }
 };
 
@@ -258,11 +288,10 @@ __device__ __forceinline__ void times4(uint4& v, uint32_t f) {
 // The loads of the last of `issued` tiles, one per stage, have landed (fixed limit).
 __device__ __forceinline__ void drain(int* abort_word, uint64_t* bars, int stages, int issued, int lane) {
     if (lane == 0) {
-        int none = 0;
-        const Waits w{&none, static_cast<uint32_t>(kWaitLimitNs)};
 #pragma unroll 1
         for (int t = max(0, issued - stages); t < issued; ++t)
-            if (!w.one(&bars[t % stages], static_cast<uint32_t>(t / stages & 1), 14)) *abort_word = 14;
+            if (!Waits::own(&bars[t % stages], static_cast<uint32_t>(t / stages & 1), static_cast<uint32_t>(kWaitLimitNs)))
+                *abort_word = 14;
     }
     __syncwarp();
 }
@@ -271,8 +300,49 @@ __device__ __forceinline__ bool bad4(uint4 v) {
     return bf16x2_bad(v.x) | bf16x2_bad(v.y) | bf16x2_bad(v.z) | bf16x2_bad(v.w);
 }
 
+// An item's query rows (its first is row q0 of the queries, `rows` of them this CTA's) by warp w
+// of n, as the K-major A operand: row r of this CTA, 16-byte piece c of its 72 (512 latent dims,
+// then 64 RoPE dims); rows that are not live are zero.
 template <bool kQ8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_latent_kernel(const Args ka, const __grid_constant__ Maps maps) {
+__device__ __forceinline__ void load_queries(const LatentArgs& a, uint32_t sQ, int64_t q0, int rows, int w, int n) {
+    const int lane = threadIdx.x & 31;
+    // a negative scale is moved to the queries: the softmax takes maxima of unscaled scores
+    const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
+    // a warp per row, two rows in flight: pieces lane, lane + 32, and in eight lanes lane + 64
+#pragma unroll 1
+    for (int r0 = w; r0 < kRows; r0 += 2 * n) {
+        uint4 x[2][3];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + k * n;
+            const uint4* lat = static_cast<const uint4*>(a.q_lat) + (q0 + r) * 64 + lane;
+            const uint4* rope = static_cast<const uint4*>(a.q_rope) + (q0 + r) * 8 + lane;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                x[k][j] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < min(rows, kRows) && (j < 2 || lane < 8)) x[k][j] = __ldg(j < 2 ? lat + 32 * j : rope);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = r0 + k * n;
+            if (r >= kRows) break;
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                uint4 v = x[k][j];
+                v = make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
+                if (kQ8 && j < 2)
+                    v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
+                                   __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
+                if (j < 2 || lane < 8)
+                    st_smem_v4(sQ + ((lane >> 3) + 4 * j) * kQSlice + r * 128 + (((lane & 7) ^ (r & 7) ^ (kQ8 && j < 2 ? lane >> 3 & 1 : 0)) << 4), v);
+            }
+        }
+    }
+}
+// kMany: several items per pair (selections over the quantised cache).
+template <bool kQ8, bool kMany>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_latent_kernel(const __grid_constant__ Args ka, const __grid_constant__ Maps maps) {
     pdl_trigger();
     using S = Smem<kQ8>;
     const LatentArgs& a = ka.a;
@@ -289,10 +359,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     // arrived on in both CTAs when a product is done: scores(t) -> bar_s[t & 1] (K stage free, scores
     // readable), aggregation(t) -> bar_o[t & 1] (V stage and P free, O updated)
     __shared__ uint64_t bar_s[2], bar_o[2], bar_final;
+    // the next item's query is in place, the last one's output is read (the even CTA's copies)
+    __shared__ uint64_t bar_query, bar_ofree;
     __shared__ float s_max[2][32 * kSmxWarps];
     __shared__ float s_sum[32 * kSmxWarps];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
+    __shared__ Item s_it;  // (drafted tokens' masks read it: no registers for it in the loops)
+    __shared__ int s_t0;
     __shared__ volatile int s_fail[2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -304,10 +378,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     const int tiles = (it.n_keys + kNK - 1) / kNK;
     const int t0 = static_cast<int>(static_cast<int64_t>(split) * tiles / ka.nsplit);
     const int nt = static_cast<int>(static_cast<int64_t>(split + 1) * tiles / ka.nsplit) - t0;
+    // the tiles of all of this pair's items are one stream for the roles (stages and barriers go on from
+    // item to item): nt of each
+    const int n_items = kMany ? (ka.items - item + ka.stride - 1) / ka.stride : 1;
+    const int all = nt * n_items;
     const Waits wait{&s_abort, wait_limit_of(a.err)};
 
     if (tid == 0) {
         s_abort = 0;
+        s_it = it;
+        s_t0 = t0;
         s_fail[0] = s_fail[1] = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar_kdone[i], kLoadWarps);
@@ -326,6 +406,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         }
         mbar_init(&bar_pfull, 2 * kSmxWarps);
         mbar_init(&bar_final, 1);
+        mbar_init(&bar_query, 4 * kLoadWarps);
+        mbar_init(&bar_ofree, 2 * kSmxWarps);
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
@@ -336,54 +418,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     const uint32_t kbase = smem_u32(sm + S::kOffK), vbase = smem_u32(sm + S::kOffV);
     const int own0 = static_cast<int>(rank) * kOwn, other0 = kOwn - own0;  // this CTA's keys of a tile, the partner's
     // keys of a tile whose rows a warp resolves: e4m3: this CTA's half and the partner's; bf16: the first
-    Rows<kQ8> keys, others;
+    Rows<kQ8, kMany> keys, others;
     if (warp >= kTmaWarp) {
         if (!kQ8 && warp == kTmaWarp && lane == 0) {
             tma_prefetch_desc(&maps.c);
             tma_prefetch_desc(&maps.cv);
             tma_prefetch_desc(&maps.kr);
         }
-        if (warp == kTmaWarp) keys.start(a, it, nt, t0 * kNK + (kQ8 ? own0 : 0) + lane);
-        if (kQ8 && warp == kTmaWarp) others.start(a, it, nt, t0 * kNK + other0 + lane);
+        if (warp == kTmaWarp) keys.start(ka, it, nt, t0 * kNK + (kQ8 ? own0 : 0) + lane);
+        if (kQ8 && warp == kTmaWarp) others.start(ka, it, nt, t0 * kNK + other0 + lane);
     } else if (warp < kTmaWarp) {
-        // the query rows, as the K-major A operand: row r of this CTA, 16-byte piece c of its 72
-        // (512 latent dims, then 64 RoPE dims); rows that are not live are zero
-        const uint32_t sQ = smem_u32(sm + S::kOffQ);
-        const int rows = it.tokens * a.H - static_cast<int>(rank) * kRows;
-        const int64_t q0 = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + rank * kRows;
-        // a negative scale is moved to the queries: the softmax takes maxima of unscaled scores
-        const uint32_t sign = a.scale < 0.f ? 0x80008000u : 0u;
-        // a warp per row, two rows in flight: pieces lane, lane + 32, and in eight lanes lane + 64
-#pragma unroll 1
-        for (int r0 = warp; r0 < kRows; r0 += 2 * kTmaWarp) {
-            uint4 x[2][3];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int r = r0 + k * kTmaWarp;
-                const uint4* lat = static_cast<const uint4*>(a.q_lat) + (q0 + r) * 64 + lane;
-                const uint4* rope = static_cast<const uint4*>(a.q_rope) + (q0 + r) * 8 + lane;
-#pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    x[k][j] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < rows && (j < 2 || lane < 8)) x[k][j] = __ldg(j < 2 ? lat + 32 * j : rope);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int r = r0 + k * kTmaWarp;
-                if (r >= kRows) break;
-#pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    uint4 v = x[k][j];
-                    v = make_uint4(v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign);
-                    if (kQ8 && j < 2)
-                        v = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.x, v.y, 0x7632),
-                                       __byte_perm(v.z, v.w, 0x5410), __byte_perm(v.z, v.w, 0x7632));
-                    if (j < 2 || lane < 8)
-                        st_smem_v4(sQ + ((lane >> 3) + 4 * j) * kQSlice + r * 128 + (((lane & 7) ^ (r & 7) ^ (kQ8 && j < 2 ? lane >> 3 & 1 : 0)) << 4), v);
-                }
-            }
-        }
+        load_queries<kQ8>(a, smem_u32(sm + S::kOffQ), (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + rank * kRows,
+                          it.tokens * a.H - static_cast<int>(rank) * kRows, warp, kTmaWarp);
         fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -397,15 +443,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     } else if (kQ8 && warp == kTmaWarp) {
         // ------------------------------------------ e4m3: pool rows and scales, as far ahead as the ring goes
 #pragma unroll 1
-        for (int h = 0; h < 2 * nt; ++h) {  // half tiles: the lanes' own keys, then the partner's
+        for (int h = 0; h < 2 * all; ++h) {  // half tiles: the lanes' own keys, then the partner's
             const int t = h >> 1, st = t % kRing, key0 = h & 1 ? other0 : own0;
             if (t >= kRing && !wait(&bar_rowsfree[st], static_cast<uint32_t>(t / kRing & 1) ^ 1, 5)) break;
             s_row[st][key0 + lane] = keys.row;
             s_scale[st][key0 + lane] = keys.sc;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_rows[st]);
-            keys.advance(a, it, nt, t0 * kNK + key0 + lane, t + 1);
-            const Rows<kQ8> x = keys;  // (one copy of the code for both)
+            keys.advance(ka, it, nt, t0 * kNK + key0 + lane);
+            const Rows<kQ8, kMany> x = keys;  // (one copy of the code for both)
             keys = others;
             others = x;
         }
@@ -420,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             uint64_t* done = v ? bar_vdone : bar_kdone;
             const uint32_t full = mapa_u32(smem_u32(v ? &bar_vfull[0] : &bar_kfull[0]), 0);
 #pragma unroll 1
-            for (int t = 0; t < nt; ++t) {
+            for (int t = 0; t < all; ++t) {
                 if (!wait.one(&done[t & 1], static_cast<uint32_t>(t >> 1 & 1), 6)) break;
                 fence_proxy_async_smem();
                 mbar_arrive_remote(full + 8 * (t & 1));
@@ -449,7 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     }
                     __syncwarp();
                     issued = t + 1;
-                    keys.advance(a, it, nt, t0 * kNK + lane, t + 1);
+                    keys.advance(ka, it, nt, t0 * kNK + lane);
                 }
                 if (t >= 1) {
                     const int u = t - 1, vs = u & 1;
@@ -493,7 +539,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         int4 row;  // pool rows (-1: none) and scale words of rows row0 .. row0 + 3
         uint4 sc;
         auto fetch = [&](int t) {
-            if (t >= nt) return true;
             const int st = t % kRing;
             if (!wait(&bar_rows[st], static_cast<uint32_t>(t / kRing & 1), 7)) return false;
             row = *reinterpret_cast<const int4*>(&s_row[st][row0]);
@@ -512,42 +557,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             if (lane == 0) mbar_arrive(&bar_rowsfree[st]);
             return true;
         };
-        bool ok = fetch(0);
+        bool ok = true;
+        int t = 0;
 #pragma unroll 1
-        for (int t = 0; ok && t < nt; ++t) {
-            const int tf = t - 2;  // the tile whose products free the stage
-            if (tf >= 0 && !wait(&freed[tf & 1], static_cast<uint32_t>(tf >> 1 & 1), 8)) break;
-            const uint32_t at = dst0 + (t & 1) * stage;
-            const bool big = __any_sync(0xffffffffu, ((sc.x | sc.y | sc.z | sc.w) & 0x80808080u) != 0);
-            const int rows[4] = {row.x, row.y, row.z, row.w};
-            const uint32_t scs[4] = {sc.x, sc.y, sc.z, sc.w};
+        for (int n = 0; ok && n < n_items; ++n) {
+            if (n > 0) {  // the next item's query, when the last scores are done
+                if (!wait(&bar_s[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 7)) break;
+                load_queries<kQ8>(a, smem_u32(sm + S::kOffQ), static_cast<int64_t>(it.b + n * ka.stride) * a.H + rank * kRows,
+                                  a.H - static_cast<int>(rank) * kRows, warp - kKWarp0, 2 * kLoadWarps);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(mapa_u32(smem_u32(&bar_query), 0));
+            }
+            ok = fetch(t);
+#pragma unroll 1
+            for (int left = nt; ok && left > 0; --left, ++t) {
+                const int tf = t - 2;  // the tile whose products free the stage
+                if (tf >= 0 && !wait(&freed[tf & 1], static_cast<uint32_t>(tf >> 1 & 1), 8)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = dst0 + (t & 1) * stage;
+                const bool big = __any_sync(0xffffffffu, ((sc.x | sc.y | sc.z | sc.w) & 0x80808080u) != 0);
+                const int rows[4] = {row.x, row.y, row.z, row.w};
+                const uint32_t scs[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t e = scs[i] >> sc_shift & 255u;
-                uint4 lo, hi;
-                convert16(u[i], rows[i] < 0 ? 0u : q8_factor_bf16x2(e), lo, hi);
-                if (big) {  // scales of 2 and above: some may need a second factor
-                    const uint32_t f2 = q8_excess_bf16x2(e);
-                    times4(lo, f2);
-                    times4(hi, f2);
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t e = scs[i] >> sc_shift & 255u;
+                    uint4 lo, hi;
+                    convert16(u[i], rows[i] < 0 ? 0u : q8_factor_bf16x2(e), lo, hi);
+                    if (big) {  // scales of 2 and above: some may need a second factor
+                        const uint32_t f2 = q8_excess_bf16x2(e);
+                        times4(lo, f2);
+                        times4(hi, f2);
+                    }
+                    const uint32_t dst = (at + i * 128) ^ (i << 4);  // (the swizzle's lower two bits)
+                    st_smem_v4(dst, lo);
+                    st_smem_v4(dst ^ 16, hi);
                 }
-                const uint32_t dst = (at + i * 128) ^ (i << 4);  // (the swizzle's lower two bits)
-                st_smem_v4(dst, lo);
-                st_smem_v4(dst ^ 16, hi);
-            }
-            if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, kr);
-            // drafted rows' non-finite pieces stay out of the aggregation
-            if (v && a.tree && (t0 + t + 1) * kNK > it.past) {
+                if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, kr);
+                // drafted rows' non-finite pieces stay out of the aggregation
+                if (v && a.tree && (s_t0 + t + 1) * kNK > s_it.past) {
 #pragma unroll 1
-                for (int i = max(0, it.past - (t0 + t) * kNK - row0); i < 4; ++i) {
-                    const uint32_t dst = (at + i * 128) ^ (i << 4);
-                    if (bad4(ld_smem_v4(dst))) st_smem_v4(dst, make_uint4(0u, 0u, 0u, 0u));
-                    if (bad4(ld_smem_v4(dst ^ 16))) st_smem_v4(dst ^ 16, make_uint4(0u, 0u, 0u, 0u));
+                    for (int i = max(0, s_it.past - (s_t0 + t) * kNK - row0); i < 4; ++i) {
+                        const uint32_t dst = (at + i * 128) ^ (i << 4);
+                        if (bad4(ld_smem_v4(dst))) st_smem_v4(dst, make_uint4(0u, 0u, 0u, 0u));
+                        if (bad4(ld_smem_v4(dst ^ 16))) st_smem_v4(dst ^ 16, make_uint4(0u, 0u, 0u, 0u));
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
+                if (left > 1) ok = fetch(t + 1);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(v ? &bar_vdone[t & 1] : &bar_kdone[t & 1]);
-            ok = fetch(t + 1);
         }
     } else if (!kQ8 && (warp == kKWarp0 || warp == kVWarp0)) {
         // ------------------------------------------ bf16 operands reported (and cleaned)
@@ -579,43 +640,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             const uint64_t pd = sdesc(smem_u32(sm + S::kOffP), 16, 1024, kSw128);
             const uint64_t vd0 = sdesc(smem_u32(sm + S::kOffV), kVSlice, 1024, kSw128);
             bool ok = true;
-            for (int t = 0; t <= nt; ++t) {
-                if (t < nt) {  // scores(t)
-                    const int sb = t & 1;
-                    ok = wait(&bar_kfull[sb], static_cast<uint32_t>(t >> 1 & 1), 3) &&
-                         (t < 2 || wait(&bar_sfree[sb], static_cast<uint32_t>(t >> 1 & 1) ^ 1, 4));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t kd = kd0 + static_cast<uint32_t>(sb * (8 * kKSlice >> 4));
-                    const uint64_t rd = rd0 + static_cast<uint32_t>(sb * (kKSlice >> 4));
-                    const uint32_t sc = tmem + kColS + 32 * sb;
-                    if (elect_one()) {
+            int g = 0;  // tiles before the item's
 #pragma unroll 1
-                        for (int sl = 0; sl < 9; ++sl) {  // 64-dim slices, 16 dims each
-                            const uint64_t qs = qd + sl * (kQSlice >> 4), ks = sl < 8 ? kd + sl * (kKSlice >> 4) : rd;
+            for (int n = 0; ok && n < n_items; ++n, g += nt) {
+                // the next item's query is in place
+                if (n > 0 && !wait(&bar_query, static_cast<uint32_t>(n & 1) ^ 1, 3)) break;
+#pragma unroll 1
+                for (int u = 0; u <= nt; ++u) {
+                    if (u < nt) {  // scores(u)
+                        const int t = g + u, sb = t & 1;
+                        ok = wait(&bar_kfull[sb], static_cast<uint32_t>(t >> 1 & 1), 3) &&
+                             (t < 2 || wait(&bar_sfree[sb], static_cast<uint32_t>(t >> 1 & 1) ^ 1, 4));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t kd = kd0 + static_cast<uint32_t>(sb * (8 * kKSlice >> 4));
+                        const uint64_t rd = rd0 + static_cast<uint32_t>(sb * (kKSlice >> 4));
+                        const uint32_t sc = tmem + kColS + 32 * sb;
+                        if (elect_one()) {
+#pragma unroll 1
+                            for (int sl = 0; sl < 9; ++sl) {  // 64-dim slices, 16 dims each
+                                const uint64_t qs = qd + sl * (kQSlice >> 4), ks = sl < 8 ? kd + sl * (kKSlice >> 4) : rd;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) mma_bf16_pair(sc, qs + 2 * i, ks + 2 * i, id_qk, (sl | i) != 0 ? 1u : 0u);
+                                for (int i = 0; i < 4; ++i) mma_bf16_pair(sc, qs + 2 * i, ks + 2 * i, id_qk, (sl | i) != 0 ? 1u : 0u);
+                            }
+                            tc_commit_pair(&bar_s[sb]);
                         }
-                        tc_commit_pair(&bar_s[sb]);
+                        __syncwarp();
                     }
-                    __syncwarp();
-                }
-                if (t > 0) {  // aggregation(t - 1)
-                    const int u = t - 1, st = u & 1;
-                    ok = wait(&bar_vfull[st], static_cast<uint32_t>(u >> 1 & 1), 5) &&
-                         wait(&bar_pfull, static_cast<uint32_t>(u & 1), 6);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t vd = vd0 + static_cast<uint32_t>(st * (kVStage >> 4));
-                    if (elect_one()) {
+                    if (u > 0) {  // aggregation(u - 1)
+                        const int t = g + u - 1, st = t & 1;
+                        ok = wait(&bar_vfull[st], static_cast<uint32_t>(t >> 1 & 1), 5) &&
+                             wait(&bar_pfull, static_cast<uint32_t>(t & 1), 6) &&
+                             (u > 1 || n == 0 || wait(&bar_ofree, static_cast<uint32_t>(n & 1) ^ 1, 6));
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = vd0 + static_cast<uint32_t>(st * (kVStage >> 4));
+                        if (elect_one()) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)  // 256 dims i / 4, 16 keys each
-                            mma_bf16_pair(tmem + kColO + 128 * (i >> 2), pd + 2 * (i & 3),
-                                          vd + (i >> 2) * (2 * kVSlice >> 4) + 128 * (i & 3), id_pv,
-                                          u > 0 || (i & 3) != 0 ? 1u : 0u);
-                        tc_commit_pair(&bar_o[u & 1]);
+                            for (int i = 0; i < 8; ++i)  // 256 dims i / 4, 16 keys each
+                                mma_bf16_pair(tmem + kColO + 128 * (i >> 2), pd + 2 * (i & 3),
+                                              vd + (i >> 2) * (2 * kVSlice >> 4) + 128 * (i & 3), id_pv,
+                                              u > 1 || (i & 3) != 0 ? 1u : 0u);
+                            tc_commit_pair(&bar_o[st]);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                 }
             }
             if (elect_one()) tc_commit_pair(&bar_final);
@@ -624,9 +693,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         // every product has finished (fixed limit), and the last arrival this CTA gets has come, before
         // the pair tears down (the even CTA's waits all have limits)
         if (lane == 0) {
-            int none = 0;
-            const Waits w{&none, static_cast<uint32_t>(rank ? 4 * kWaitLimitNs : kWaitLimitNs)};
-            if (!w.one(&bar_final, 0, 12)) s_abort = 12;
+            if (!Waits::own(&bar_final, 0, static_cast<uint32_t>(rank ? 4 * kWaitLimitNs : kWaitLimitNs))) s_abort = 12;
         }
         __syncwarp();
     }
@@ -634,189 +701,221 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         // ---------------------------------------------- softmax + output
         // row of this CTA; the row's half of the keys (and of the output dims), by tensor-memory lane; quarter of them
         const int r = tid & 63, hf = tid >> 6 & 1, qd = tid >> 7;
-        const int m_row = static_cast<int>(rank) * kRows + r;
-        const bool live = m_row < it.tokens * a.H;
-        const int token = it.i0 + (live ? m_row / a.H : 0);
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t sfree0 = mapa_u32(smem_u32(&bar_sfree[0]), 0), pfull0 = mapa_u32(smem_u32(&bar_pfull), 0);
         const uint32_t prow = smem_u32(sm + S::kOffP) + r * 128;
         // scores in base-2 units (the queries carry the sign; never 0, so that masked scores stay -inf)
         const float c2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-37f);
-        float m = -INFINITY, l = 0.f;
         bool ok = true;
-        // which of the 32 keys of this thread's half of tile t its row attends to.  Selections: the
-        // slots of eight tiles are loaded eight tiles ahead (the fence that
-        // publishes P waits for loads in flight); lane u holds tile u's mask.
-        int slots[8];
+        // which of this thread's 16 keys of the item's tile t its row attends to.  Selections: the
+        // slots of eight tiles are loaded eight tiles ahead (the fence that publishes P waits for
+        // loads in flight): the half's 32 of a tile per load, lane u holding tile u's mask, or, with
+        // registers short (kMany), this thread's 16 of two tiles, lane u holding tiles 2 u and 2 u + 1.
+        constexpr int kLoads = kMany ? 4 : 8;
+        int slots[kLoads];
         uint32_t vis8 = 0;
-        auto load_slots = [&](int t) {
+        auto load_slots = [&](int n, int t) {  // of the pair's n-th item
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int s = (t0 + t + u) * kNK + hf * 32 + lane;
-                slots[u] = t + u < nt && s < a.k ? a.idx[static_cast<int64_t>(it.b) * a.k + s] : -1;
+            for (int u = 0; u < kLoads; ++u) {
+                const int tile = kMany ? t + 2 * u + (lane >> 4) : t + u;
+                const int s = (s_t0 + tile) * kNK + hf * 32 + (kMany ? qd * 16 + (lane & 15) : lane);
+                slots[u] = tile < nt && s < a.k ? a.idx[static_cast<int64_t>(s_it.b + n * ka.stride) * a.k + s] : -1;
             }
         };
-        auto next_slots = [&](int t) {
+        auto next_slots = [&](int n, int t) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < kLoads; ++u) {
                 const uint32_t v = __ballot_sync(0xffffffffu, slots[u] >= 0);
                 if (lane == u) vis8 = v;
             }
-            load_slots(t + 8);
+            load_slots(n, t + 8);
         };
-        auto visible = [&](int t) -> uint32_t {
-            const int s0 = (t0 + t) * kNK + hf * 32;
+        auto visible = [&](int n, int t) -> uint32_t {
             if (a.idx) {
-                if ((t & 7) == 0) next_slots(t);
-                return __shfl_sync(0xffffffffu, vis8, t & 7);
+                if ((t & 7) == 0) next_slots(n, t);
+                if (kMany) return __shfl_sync(0xffffffffu, vis8, t >> 1 & 3) >> (16 * (t & 1)) & 0xFFFFu;
+                return __shfl_sync(0xffffffffu, vis8, t & 7) >> (16 * qd) & 0xFFFFu;
             }
-            if (s0 + 32 <= it.past) return 0xffffffffu;
-            uint32_t v = s0 < it.past ? (1u << (it.past - s0)) - 1u : 0u;
-            const int n = min(32, it.n_keys - s0);
-            const uint8_t* mk = a.tree_mask ? a.tree_mask + (static_cast<int64_t>(it.b) * a.T + token) * a.T : nullptr;
+            const int s0 = (s_t0 + t) * kNK + hf * 32 + qd * 16, past = s_it.past;
+            if (s0 + 16 <= past) return 0xFFFFu;
+            const int m_row = static_cast<int>(cluster_rank()) * kRows + r;
+            const int token = s_it.i0 + (m_row < s_it.tokens * a.H ? m_row / a.H : 0);
+            uint32_t v = s0 < past ? (1u << (past - s0)) - 1u : 0u;
+            const int keys = min(16, s_it.n_keys - s0);
+            const uint8_t* mk = a.tree_mask ? a.tree_mask + (static_cast<int64_t>(s_it.b) * a.T + token) * a.T : nullptr;
 #pragma unroll 1
-            for (int j = max(0, it.past - s0); j < n; ++j) {
-                const int d = s0 + j - it.past;
+            for (int j = max(0, past - s0); j < keys; ++j) {
+                const int d = s0 + j - past;
                 if (mk ? mk[d] != 0 : d <= token) v |= 1u << j;
             }
             return v;
         };
-        if (a.idx) load_slots(0);
+        if (a.idx) load_slots(0, 0);
+        int t = 0;  // of the pair's tiles
 #pragma unroll 1
-        for (int t = 0; t < nt; ++t) {
-            const int sb = t & 1;
-            const uint32_t vis = visible(t) >> (16 * qd) & 0xFFFFu;
-            ok = ok && wait(&bar_s[sb], static_cast<uint32_t>((t >> 1) & 1), 8);
-            float s[16];
-            if (ok) {
+        for (int n = 0; n < n_items; ++n) {
+            float m = -INFINITY, l = 0.f;
+            bool failed = false;
+#pragma unroll 1
+            for (int u = 0; u < nt; ++u, ++t) {
+                const int sb = t & 1;
+                const uint32_t vis = visible(n, u);
+                ok = ok && wait(&bar_s[sb], static_cast<uint32_t>((t >> 1) & 1), 8);
+                float s[16];
+                if (ok) {
+                    tc_fence_after();
+                    uint32_t v[16];
+                    tmem_ld16(tmem + lane_base + kColS + 32 * sb + 16 * qd, v);
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(sfree0 + 8 * sb);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = __uint_as_float(v[j]);
+                    if (!__all_sync(0xffffffffu, vis == 0xFFFFu)) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (!(vis >> j & 1u)) s[j] = -INFINITY;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) s[j] = -INFINITY;
+                    if (lane == 0) s_fail[sb] = 1;
+                }
+                const float mx = tree_max(s) * c2;
+                s_max[sb][tid] = mx;
+                named_sync(1, 32 * kSmxWarps);
+                // a failed wait before this barrier is seen by all four warps after it (the flag
+                // of the next tile is another word), so they leave the loop together
+                if (s_fail[sb]) {
+                    ok = false;
+                    failed = true;
+                    break;
+                }
+                const float top = fmaxf(fmaxf(mx, s_max[sb][tid ^ 64]), fmaxf(s_max[sb][tid ^ 128], s_max[sb][tid ^ 192]));
+                const bool grow = top > m + kRescaleLog2;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float m_new = grow ? top : m;
+                    const float alpha = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - m_new)) : 1.f;
+                    if (u > 0) {  // O holds the item's tiles before this one
+                        ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 9);
+                        if (ok) {
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 128 * qd; c < 128 * qd + 128; c += 32) {
+                                uint32_t o[32];
+                                tmem_ld32(tmem + lane_base + kColO + c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                                tmem_st32(tmem + lane_base + kColO + c, o);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+                    l *= alpha;
+                    m = m_new;
+                }
+                const float mref = m == -INFINITY ? 0.f : m;  // masked keys are -inf and give exactly 0
+                uint32_t pk[8];
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p0 = fast_exp2(s[2 * j] * c2 - mref), p1 = fast_exp2(s[2 * j + 1] * c2 - mref);
+                    sum += p0 + p1;
+                    pk[j] = pack_bf16x2(p0, p1);
+                }
+                l += sum;
+                // aggregation(t - 1) has read P
+                if (ok && t > 0)
+                    ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 10);
+                if (ok) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        st_smem_v4(prow + (((4 * hf + 2 * qd + q) ^ (r & 7)) << 4),
+                                   make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
+                    fence_proxy_async_smem();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(pfull0);
+                }
+            }
+            // ---- the row's sums, then the rows out: staged over the idle operands, bulk copies
+            s_sum[tid] = l;
+            named_sync(1, 32 * kSmxWarps);
+            l = (s_sum[r] + s_sum[r + 64]) + (s_sum[r + 128] + s_sum[r + 192]);  // (one order in all four)
+            const int m_row = static_cast<int>(cluster_rank()) * kRows + r;
+            const bool live = m_row < s_it.tokens * a.H;
+            const int64_t orow = (static_cast<int64_t>(s_it.b + n * ka.stride) * a.T + s_it.i0) * a.H + m_row;
+            const bool last = n + 1 == n_items;
+            uint8_t* dst = nullptr;
+            if (ok && nt > 0)
+                ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 11);
+            if (ok && !*wait.abort) {
                 tc_fence_after();
-                uint32_t v[16];
-                tmem_ld16(tmem + lane_base + kColS + 32 * sb + 16 * qd, v);
-                tmem_ld_wait();
+                const bool partial = ka.nsplit > 1;
+                const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
+                const bool empty = l == 0.f;  // (a NaN sum is not empty)
+                const float inv = empty || partial ? 1.f : 1.f / l;
+                const bool bf = !partial && a.out_bf16 != nullptr;
+                dst = partial ? reinterpret_cast<uint8_t*>(ka.ws_o + wrow * 512)
+                              : (bf ? static_cast<uint8_t*>(a.out_bf16) + orow * 1024 : reinterpret_cast<uint8_t*>(a.out + orow * 512));
+                // a thread's 128 dims: the last item's staged over the idle operands (bulk copies), the others', while
+                // the next item's tiles are under way, straight to memory
+                uint8_t* to = last ? sm + r * kORow : dst;
+#pragma unroll 1
+                for (int c = 128 * qd; c < 128 * qd + 128; c += kMany ? 16 : 32) {
+                    const int d = qd * 256 + hf * 128 + (c & 127);
+                    const int swap = kQ8 ? (c & 64) >> 3 : 0;  // groups of eight dims are swapped in odd slices
+                    constexpr int kCols = kMany ? 16 : 32;
+                    uint32_t o[kCols];
+                    if (nt > 0) {
+                        if constexpr (kMany)
+                            tmem_ld16(tmem + lane_base + kColO + c, o);
+                        else
+                            tmem_ld32(tmem + lane_base + kColO + c, o);
+                        tmem_ld_wait();
+                    }
+                    if (!live) continue;
+#pragma unroll
+                    for (int j = 0; j < kCols; j += 8) {
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int at = kQ8 && ((i & 3) == 1 || (i & 3) == 2) ? i ^ 3 : i;  // dims in the order 0, 2, 1, 3
+                            f[i] = empty ? 0.f : __uint_as_float(o[j + at]) * inv;
+                        }
+                        if (bf) {
+                            *reinterpret_cast<uint4*>(to + 2 * (d + (j ^ swap))) =
+                                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                        } else {
+                            float4* at = reinterpret_cast<float4*>(to + 4 * (d + (j ^ swap)));
+                            at[0] = make_float4(f[0], f[1], f[2], f[3]);
+                            at[1] = make_float4(f[4], f[5], f[6], f[7]);
+                        }
+                    }
+                }
+                if (live && tid < kRows) {
+                    if (partial)
+                        *reinterpret_cast<float2*>(ka.ws_ml + wrow * 2) = make_float2(m, l);
+                    else if (a.lse)
+                        a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster_relaxed(sfree0 + 8 * sb);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[j] = __uint_as_float(v[j]);
-                if (!__all_sync(0xffffffffu, vis == 0xFFFFu)) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (!(vis >> j & 1u)) s[j] = -INFINITY;
+                if (kMany && lane == 0) mbar_arrive_cluster_relaxed(mapa_u32(smem_u32(&bar_ofree), 0));  // O is read
+                if (last) fence_proxy_async_smem();
+            }
+            if (failed) break;  // (all eight warps)
+            if (last) {
+                named_sync(1, 32 * kSmxWarps);  // the threads of a row have staged it (one bulk copy per row)
+                if (ok && !*wait.abort && live && tid < kRows) {
+                    bulk_copy_s2g(dst, sm + r * kORow, ka.nsplit == 1 && a.out_bf16 ? 1024 : 2048);
+                    bulk_wait_all();
                 }
             } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) s[j] = -INFINITY;
-                if (lane == 0) s_fail[sb] = 1;
+                load_slots(n + 1, 0);
             }
-            const float mx = tree_max(s) * c2;
-            s_max[sb][tid] = mx;
-            named_sync(1, 32 * kSmxWarps);
-            // a failed wait before this barrier is seen by all four warps after it (the flag
-            // of the next tile is another word), so they leave the loop together
-            if (s_fail[sb]) {
-                ok = false;
-                break;
-            }
-            const float top = fmaxf(fmaxf(mx, s_max[sb][tid ^ 64]), fmaxf(s_max[sb][tid ^ 128], s_max[sb][tid ^ 192]));
-            const bool grow = top > m + kRescaleLog2;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float m_new = grow ? top : m;
-                const float alpha = grow ? (m == -INFINITY ? 0.f : fast_exp2(m - m_new)) : 1.f;
-                if (t > 0) {  // O holds the tiles before t
-                    ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 9);
-                    if (ok) {
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 128 * qd; c < 128 * qd + 128; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tmem + lane_base + kColO + c, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                            tmem_st32(tmem + lane_base + kColO + c, o);
-                        }
-                        tmem_st_wait();
-                    }
-                }
-                l *= alpha;
-                m = m_new;
-            }
-            const float mref = m == -INFINITY ? 0.f : m;  // masked keys are -inf and give exactly 0
-            uint32_t pk[8];
-            float sum = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float p0 = fast_exp2(s[2 * j] * c2 - mref), p1 = fast_exp2(s[2 * j + 1] * c2 - mref);
-                sum += p0 + p1;
-                pk[j] = pack_bf16x2(p0, p1);
-            }
-            l += sum;
-            // aggregation(t - 1) has read P
-            if (ok && t > 0)
-                ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 10);
-            if (ok) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    st_smem_v4(prow + (((4 * hf + 2 * qd + q) ^ (r & 7)) << 4),
-                               make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
-                fence_proxy_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(pfull0);
-            }
-        }
-        // ---- the row's sums, then the rows out: staged over the idle operands, bulk copies
-        s_sum[tid] = l;
-        named_sync(1, 32 * kSmxWarps);
-        l = (s_sum[r] + s_sum[r + 64]) + (s_sum[r + 128] + s_sum[r + 192]);  // (one order in all four)
-        if (ok && nt > 0)
-            ok = wait(&bar_o[(nt - 1) & 1], static_cast<uint32_t>((nt - 1) >> 1 & 1), 11);
-        if (ok && !*wait.abort) {
-            tc_fence_after();
-            const bool partial = ka.nsplit > 1;
-            const bool bf = !partial && a.out_bf16 != nullptr;
-            const bool empty = l == 0.f;  // (a NaN sum is not empty)
-            const float inv = empty || partial ? 1.f : 1.f / l;
-            uint8_t* srow = sm + r * kORow;
-#pragma unroll 1
-            for (int c = 128 * qd; c < 128 * qd + 128; c += 32) {
-                const int d = qd * 256 + hf * 128 + (c & 127);
-                const int swap = kQ8 ? (c & 64) >> 3 : 0;  // groups of eight dims are swapped in odd slices
-                uint32_t o[32];
-                if (nt > 0) {
-                    tmem_ld32(tmem + lane_base + kColO + c, o);
-                    tmem_ld_wait();
-                }
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    float f[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int n = kQ8 && (i == 1 || i == 2) ? 3 - i : i;  // dims in the order 0, 2, 1, 3
-                        f[i] = empty ? 0.f : __uint_as_float(o[j + n]) * inv;
-                    }
-                    if (bf)
-                        *reinterpret_cast<uint2*>(srow + 2 * (d + (j ^ swap))) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-                    else
-                        *reinterpret_cast<float4*>(srow + 4 * (d + (j ^ swap))) = make_float4(f[0], f[1], f[2], f[3]);
-                }
-            }
-            fence_proxy_async_smem();
-        }
-        named_sync(1, 32 * kSmxWarps);  // the threads of a row have staged it (one bulk copy per row)
-        if (ok && !*wait.abort && live && tid < kRows) {
-            const bool partial = ka.nsplit > 1;
-            const int64_t orow = (static_cast<int64_t>(it.b) * a.T + it.i0) * a.H + m_row;
-            const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
-            uint8_t* dst = partial ? reinterpret_cast<uint8_t*>(ka.ws_o + wrow * 512)
-                                   : (a.out_bf16 ? static_cast<uint8_t*>(a.out_bf16) + orow * 1024
-                                                 : reinterpret_cast<uint8_t*>(a.out + orow * 512));
-            bulk_copy_s2g(dst, sm + r * kORow, !partial && a.out_bf16 ? 1024 : 2048);
-            if (partial)
-                *reinterpret_cast<float2*>(ka.ws_ml + wrow * 2) = make_float2(m, l);
-            else if (a.lse)
-                a.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-            bulk_wait_all();
         }
     }
 
@@ -900,7 +999,7 @@ int splits(int64_t items, int k) {
 
 size_t state_bytes(int64_t items, int ns) { return static_cast<size_t>(items) * ns * 128 * (512 + 2) * 4; }
 
-template <bool kQ8>
+template <bool kQ8, bool kMany>
 sa_status launch(const Args& ka, int64_t items, cudaStream_t st) {
     const LatentArgs& a = ka.a;
     Maps maps = {};
@@ -914,9 +1013,10 @@ sa_status launch(const Args& ka, int64_t items, cudaStream_t st) {
             !encode_tiled(&maps.kr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.kr_cache, rdims, rstride, half, CU_TENSOR_MAP_SWIZZLE_128B))
             return SA_ECUDA;
     }
-    const cudaError_t e = cudaFuncSetAttribute(mla_latent_kernel<kQ8>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kQ8>::kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(mla_latent_kernel<kQ8, kMany>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<kQ8>::kBytes);
     if (e != cudaSuccess) return launch_status(e);
-    mla_latent_kernel<kQ8><<<static_cast<unsigned>(2 * items * ka.nsplit), kThreads, Smem<kQ8>::kBytes, st>>>(ka, maps);
+    const int64_t clusters = kMany ? ka.stride : items * ka.nsplit;
+    mla_latent_kernel<kQ8, kMany><<<static_cast<unsigned>(2 * clusters), kThreads, Smem<kQ8>::kBytes, st>>>(ka, maps);
     return launch_status(cudaGetLastError());
 }
 
@@ -936,12 +1036,25 @@ sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cuda
     ka.groups = (a.T + ka.tokens_per_item - 1) / ka.tokens_per_item;
     const int64_t items = static_cast<int64_t>(a.B) * ka.groups;
     ka.nsplit = splits(items, a.k);
+    ka.items = static_cast<int>(items);
+    // Short selections, more of them than pairs, go to the pairs in turn (equal tiles each), so that an item's
+    // query and first rows load behind the output before: 500 rows x 128 heads of 64 / 256 / 512 slots take
+    // 78 / 115 / 170 us against 100 / 137 / 184 with a pair for each, 768 the same, 1024 285 against 273 (a tile
+    // takes 2.0 us there against 1.56: the loops around the tiles' cost registers); 100 rows of 64 / 200 / 400
+    // 25 / 37 / 49 against 27 / 38 / 48.
+    if (a.idx && ka.nsplit == 1) {
+        const int64_t pairs = sm_count() / 2, tiles = (a.k + kNK - 1) / kNK;
+        // (the end of a pair's work is waited for with a limit: some 4000 items, 60 ms, a pair at most)
+        if (items > pairs && (tiles <= 4 || (tiles <= 8 && items > 2 * pairs)))
+            ka.stride = static_cast<int>(std::max(pairs, (items + 4095) / 4096));
+    }
     if (ka.nsplit > 1) {
         if (!ws || ws_bytes < state_bytes(items, ka.nsplit)) return SA_EINVAL;
         ka.ws_o = static_cast<float*>(ws);
         ka.ws_ml = ka.ws_o + static_cast<size_t>(items) * ka.nsplit * 128 * 512;
     }
-    const sa_status s = a.c_scale ? launch<true>(ka, items, st) : launch<false>(ka, items, st);
+    const sa_status s = !a.c_scale ? launch<false, false>(ka, items, st)
+                        : ka.stride ? launch<true, true>(ka, items, st) : launch<true, false>(ka, items, st);
     if (s == SA_OK && ka.nsplit > 1) {
         const int64_t rows = static_cast<int64_t>(a.B) * a.T * a.H;
         constexpr int kPer = kCombThreads / 128;

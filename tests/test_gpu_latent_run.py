@@ -256,6 +256,71 @@ def test_an_overflowing_drafted_row_stays_with_its_tokens():
         check_attention(out[0, i], None, attend64(q[0, i], qr[0, i], cache, 0, pos), f"token {i}")
 
 
+def many(rows, H, k, seed):
+    """`rows` selections of up to k positions of five sequences, with empty slots and empty rows."""
+    lens = (900, 64, 333, 1, 2000)
+    cache = make_cache(lens, True, seed, DEV, junk_nan=True)
+    rng = np.random.Generator(np.random.PCG64(seed))
+    seq = rng.integers(0, 5, rows)
+    idx = np.full((rows, k), -1, dtype=np.int64)
+    for r in range(rows):
+        m = min(k, lens[seq[r]])
+        idx[r, :m] = rng.permutation(lens[seq[r]])[:m]
+        idx[r, rng.random(k) < 0.1] = -1
+    idx[::7] = -1
+    g = gen(seed, DEV)
+    q = torch.randn(rows, H, D_C, generator=g, device=DEV).bfloat16()
+    qr = torch.randn(rows, H, D_R, generator=g, device=DEV).bfloat16()
+    return cache, seq, idx, q, qr
+
+
+@pytest.mark.parametrize("bf16_out", [False, True])
+@pytest.mark.parametrize("rows,H,k", [(75, 128, 1), (149, 64, 200), (400, 33, 130), (1000, 8, 512), (230, 128, 513)])
+def test_more_short_selections_than_the_gpu_has_sms(rows, H, k, bf16_out):
+    """Rows that share an SM pair one after the other (and, with 513 slots, do not), each against fp64."""
+    cache, seq, idx, q, qr = many(rows, H, k, rows)
+    out = torch.full((rows, H, D_C), torch.nan, device=DEV, dtype=torch.bfloat16 if bf16_out else torch.float32)
+    lse = torch.full((rows, H), torch.nan, device=DEV)
+
+    def call():
+        sa.sparse_mla_prefill(q, qr, cache["c_cache"], cache["kr_cache"], ints(idx), SCALE, cache["pps"],
+                              page_table=cache["page_table"], seq_of_row=ints(seq), out=out, lse=lse,
+                              c_scale=cache["c_scale"])
+
+    call()
+    for r in range(rows):
+        check_attention(out[r], lse[r], attend64(q[r], qr[r], cache, seq[r], idx[r][idx[r] >= 0]), f"row {r}")
+    first = out.clone(), lse.clone()
+    for _ in range(10):
+        call()
+    assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    assert sa.check_device_error() == 0
+
+
+def test_wait_limit_runs_out_between_rows_of_a_pair():
+    """As below, where several rows share an SM pair."""
+    cache, seq, idx, q, qr = many(300, 64, 100, 3)
+
+    def call():
+        return sa.sparse_mla_decode(q, qr, cache["c_cache"], cache["kr_cache"], ints(idx), SCALE, cache["pps"],
+                                    page_table=cache["page_table"], seq_of_row=ints(seq), c_scale=cache["c_scale"])
+
+    call()
+    assert sa.check_device_error() == 0
+    sa.set_wait_limit_ns(200)
+    try:
+        call()
+        torch.cuda.synchronize()
+        code = sa.check_device_error()
+    finally:
+        sa.set_wait_limit_ns(0)
+    assert code & 0xF00 == 0xA00, f"expected a latent-attention wait site, got 0x{code:x}"
+    out = call()
+    assert sa.check_device_error() == 0
+    for r in range(0, 300, 11):
+        check_attention(out[r], None, attend64(q[r], qr[r], cache, seq[r], idx[r][idx[r] >= 0]), f"row {r}")
+
+
 def test_broadcast_token_rows_are_refused():
     """Rows of the written tokens that overlap (stride 0) are not a layout the write reads."""
     cache = make_cache((64, 64), True, 2, DEV)
