@@ -863,11 +863,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 // a thread's 128 dims: the last item's staged over the idle operands (bulk copies), the others', while
                 // the next item's tiles are under way, straight to memory
                 uint8_t* to = last ? sm + r * kORow : dst;
+                constexpr int kCols = kMany ? 16 : 32;
 #pragma unroll 1
-                for (int c = 128 * qd; c < 128 * qd + 128; c += kMany ? 16 : 32) {
+                for (int c = 128 * qd; c < 128 * qd + 128; c += kCols) {
                     const int d = qd * 256 + hf * 128 + (c & 127);
                     const int swap = kQ8 ? (c & 64) >> 3 : 0;  // groups of eight dims are swapped in odd slices
-                    constexpr int kCols = kMany ? 16 : 32;
                     uint32_t o[kCols];
                     if (nt > 0) {
                         if constexpr (kMany)
@@ -876,24 +876,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                             tmem_ld32(tmem + lane_base + kColO + c, o);
                         tmem_ld_wait();
                     }
-                    if (!live) continue;
+                    if (live) {
 #pragma unroll
-                    for (int j = 0; j < kCols; j += 8) {
-                        float f[8];
+                        for (int j = 0; j < kCols; j += 8) {
+                            float f[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int at = kQ8 && ((i & 3) == 1 || (i & 3) == 2) ? i ^ 3 : i;  // dims in the order 0, 2, 1, 3
-                            f[i] = empty ? 0.f : __uint_as_float(o[j + at]) * inv;
-                        }
-                        if (bf) {
-                            *reinterpret_cast<uint4*>(to + 2 * (d + (j ^ swap))) =
-                                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-                        } else {
-                            float4* at = reinterpret_cast<float4*>(to + 4 * (d + (j ^ swap)));
-                            at[0] = make_float4(f[0], f[1], f[2], f[3]);
-                            at[1] = make_float4(f[4], f[5], f[6], f[7]);
+                            for (int i = 0; i < 8; ++i) {
+                                const int at = kQ8 && ((i & 3) == 1 || (i & 3) == 2) ? i ^ 3 : i;  // dims in the order 0, 2, 1, 3
+                                f[i] = empty ? 0.f : __uint_as_float(o[j + at]) * inv;
+                            }
+                            if (bf) {
+                                *reinterpret_cast<uint4*>(to + 2 * (d + (j ^ swap))) =
+                                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+                            } else {
+                                float4* at = reinterpret_cast<float4*>(to + 4 * (d + (j ^ swap)));
+                                at[0] = make_float4(f[0], f[1], f[2], f[3]);
+                                at[1] = make_float4(f[4], f[5], f[6], f[7]);
+                            }
                         }
                     }
+                    __syncwarp();  // (the loads are the whole warp's)
                 }
                 if (live && tid < kRows) {
                     if (partial)
