@@ -51,6 +51,7 @@
 
 #include "sa_device.cuh"
 #include "sa_internal.h"
+#include "sa_wait.h"
 
 namespace sa {
 namespace {
@@ -127,7 +128,7 @@ struct Waits {
 #pragma unroll 1
         while (!mbar_try_wait(b, parity)) {
             if (*abort) return false;
-            if (now() - t0 > limit_ns) {
+            if (wait32_over(t0, now(), limit_ns)) {
                 *abort = site;
                 return false;
             }
@@ -139,7 +140,7 @@ struct Waits {
         const uint32_t t0 = now();
 #pragma unroll 1
         while (!mbar_try_wait(b, parity))
-            if (now() - t0 > limit_ns) return false;
+            if (wait32_over(t0, now(), limit_ns)) return false;
         return true;
     }
     // The whole warp leaves together.
@@ -382,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     // item to item): nt of each
     const int n_items = kMany ? (ka.items - item + ka.stride - 1) / ka.stride : 1;
     const int all = nt * n_items;
-    const Waits wait{&s_abort, wait_limit_of(a.err)};
+    const Waits wait{&s_abort, wait32_limit(wait_limit_of(a.err))};
 
     if (tid == 0) {
         s_abort = 0;
@@ -693,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         // every product has finished (fixed limit), and the last arrival this CTA gets has come, before
         // the pair tears down (the even CTA's waits all have limits)
         if (lane == 0) {
-            if (!Waits::own(&bar_final, 0, static_cast<uint32_t>(rank ? 4 * kWaitLimitNs : kWaitLimitNs))) s_abort = 12;
+            if (!Waits::own(&bar_final, 0, static_cast<uint32_t>(rank ? 3 * kWaitLimitNs : kWaitLimitNs))) s_abort = 12;
         }
         __syncwarp();
     }
