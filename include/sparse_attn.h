@@ -606,7 +606,8 @@ sa_status sa_dense_mla_q8(const void* q_lat, const void* q_rope, const void* c_c
  *   bf16; lse [B][T][H] fp32 or NULL.  Rows i >= n_draft[b] are not written.
  *   seq_of_row [B]: the sequence of tree b (NULL: b).  A token with nothing to
  *   attend to gets zeros and lse -inf.  Masked rows never reach a result, NaN or
- *   infinite contents included.
+ *   infinite contents included; a token that sees a drafted row with a NaN or an
+ *   infinity among its latent values gets NaN in its output and lse.
  *   L_max >= n_past[b] + n_draft[b] for every b sets the key split and the
  *   workspace; a longer sequence still gives right results.
  * cache_dtype SA_BF16 (c_scale NULL, c_ld in elements) or SA_E4M3.

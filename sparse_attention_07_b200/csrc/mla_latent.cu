@@ -29,8 +29,9 @@
 //  * One thread of the even CTA issues scores(t + 1) before aggregation(t).
 //  * Drafted rows are masked token by token, so a row that some token must not see
 //    may be in the tile; non-finite contents of such a row are zeroed in the
-//    aggregation operand (0 * NaN would reach every token).  Tokens that see the
-//    row still get NaN, through its scores.
+//    aggregation operand (0 * NaN would reach every token) and NaN in the score
+//    operand (an infinity alone can score -inf, as if masked): the tokens that see
+//    the row get NaN, through its score.
 //  * Few items split their keys over several pairs; partial states go to a
 //    workspace and a combine kernel merges them in split order.
 //  * Many short selections go to the pairs in turn (kMany): the tiles of a pair's items
@@ -299,6 +300,12 @@ __device__ __forceinline__ void drain(int* abort_word, uint64_t* bars, int stage
 
 __device__ __forceinline__ bool bad4(uint4 v) {
     return bf16x2_bad(v.x) | bf16x2_bad(v.y) | bf16x2_bad(v.z) | bf16x2_bad(v.w);
+}
+
+// A 16-byte piece of a drafted row's operand, of the aggregation (v) or of the scores.
+__device__ __forceinline__ void clean_piece(uint32_t at, bool v) {
+    const uint32_t w = v ? 0u : 0x7FC07FC0u;
+    if (bad4(ld_smem_v4(at))) st_smem_v4(at, make_uint4(w, w, w, w));
 }
 
 // An item's query rows (its first is row q0 of the queries, `rows` of them this CTA's) by warp w
@@ -597,13 +604,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     st_smem_v4(dst ^ 16, hi);
                 }
                 if (!v) st_smem_v4(rdst + (t & 1) * kKSlice, kr);
-                // drafted rows' non-finite pieces stay out of the aggregation
-                if (v && a.tree && (s_t0 + t + 1) * kNK > s_it.past) {
+                // drafted rows' non-finite pieces (codes reach 448: only with scales above 1) stay out of the
+                // aggregation and are NaN in the scores
+                if (big && a.tree && (s_t0 + t + 1) * kNK > s_it.past) {
 #pragma unroll 1
                     for (int i = max(0, s_it.past - (s_t0 + t) * kNK - row0); i < 4; ++i) {
                         const uint32_t dst = (at + i * 128) ^ (i << 4);
-                        if (bad4(ld_smem_v4(dst))) st_smem_v4(dst, make_uint4(0u, 0u, 0u, 0u));
-                        if (bad4(ld_smem_v4(dst ^ 16))) st_smem_v4(dst ^ 16, make_uint4(0u, 0u, 0u, 0u));
+                        clean_piece(dst, v);
+                        clean_piece(dst ^ 16, v);
                     }
                 }
                 __syncwarp();
@@ -619,12 +627,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         for (int t = 0; t < nt; ++t) {
             const int st = t & 1;
             if (!wait(&landed[st], static_cast<uint32_t>(t >> 1 & 1), 13)) break;
-            const int tile0 = (t0 + t) * kNK;
-            if (v && tile0 + kNK > it.past) {  // lane = 16-byte piece of a row
-                for (int j = max(0, it.past - tile0); j < kNK; ++j) {
-                    const uint32_t at = vbase + st * kVStage + (lane >> 3) * kVSlice + j * 128 + (((lane & 7) ^ (j & 7)) << 4);
-                    if (bad4(ld_smem_v4(at))) st_smem_v4(at, make_uint4(0u, 0u, 0u, 0u));
-                }
+            const int pos0 = (t0 + t) * kNK + (v ? 0 : own0);  // of the operand's row 0
+            if ((t0 + t + 1) * kNK > it.past) {  // lane = 16-byte pieces of a row
+                const uint32_t at0 = v ? vbase + st * kVStage : kbase + st * 8 * kKSlice, slice = v ? kVSlice : kKSlice;
+                const int rows = v ? kNK : min(kOwn, it.n_keys - pos0);  // (scores of keys past the last are masked)
+                for (int j = max(0, it.past - pos0); j < rows; ++j)
+                    for (int p = lane; p < (v ? 32 : 64); p += 32)
+                        clean_piece(at0 + (p >> 3) * slice + j * 128 + (((p & 7) ^ (j & 7)) << 4), v);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
