@@ -501,7 +501,9 @@ sa_status sa_topk_from_candidates(const uint64_t* cand, int64_t cand_ld, int32_t
  *     out[a] = y[a] cos - y[b] sin;  out[b] = y[b] cos + y[a] sin
  * pairs (i, i + rope_dims/2), or (2i, 2i+1) when interleaved != 0, with
  * cos, sin [n_pos][rope_dims/2] fp32 read at row positions[token].  All in
- * fp32, rounded once to the storage type.
+ * fp32, rounded once to the storage type; finite rows of any size are normalised
+ * (where the sum of squares leaves fp32's range, of the row scaled).  norm == 0:
+ * y = x * weight.
  *   q [tokens][H_q][D], k [tokens][H_k][D], dtype SA_BF16 or SA_F32, element
  *   strides per token and head given, dims contiguous; outputs likewise (out may
  *   be the input itself; any other overlap is undefined).  H_k = 0 or H_q = 0:
@@ -525,7 +527,7 @@ sa_status sa_qk_norm_rope(const void* q, int64_t q_token_stride, int64_t q_head_
  * written before it is read).  For token t with slots[t] >= 0 (negative: a
  * padded token, nothing is written), at the pool row of position slots[t] of
  * sequence seq_of_row[t]:
- *   latent   y = c * rsqrt(mean(c^2) + eps) * weight   (norm == 0: y = c)
+ *   latent   y = c * rsqrt(mean(c^2) + eps) * weight   (norm == 0: y = c * weight)
  *            stored as bf16 (cache_dtype SA_BF16, c_scale NULL), or as e4m3
  *            codes (SA_E4M3) with one scale byte per 128 dims in c_scale
  *            [pool_pages*64][scale_ld]: byte e stands for 2^(e-127), the smallest

@@ -102,7 +102,15 @@ __global__ void __launch_bounds__(kThreads) mla_cache_write_kernel(const CacheWr
         for (int j = 0; j < 16; ++j) ss += v[j] * v[j];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        r = rsqrtf(ss * (1.f / kDc) + a.eps);
+        const float f = norm_factor(ss * (1.f / kDc), a.eps);
+        if (f != 1.f) {  // (of the whole warp alike)
+            ss = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] *= f, ss += v[j] * v[j];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
+        r = rsqrtf(ss * (1.f / kDc) + a.eps * f * f);
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = v[j] * r * w[j];

@@ -9,12 +9,13 @@
 //
 // Bound by HBM on chunks (each element read once and written once) and by
 // launch and load latency on a decode step.  A lane owns two pieces of four
-// consecutive dims of a head, each piece one load: for split pairs the piece at d and the one at d + rot/2, so both dims of a pair are in
-// the lane that rotates them, with no shuffle, no second load, and a call in
-// place needs no ordering between lanes.  The cos/sin and weight values of a
+// consecutive dims of a head, each piece one load: for split pairs the piece at
+// d and the one at d + rot/2, so both dims of a pair are in the lane that rotates
+// them, with no shuffle, no second load, and a call in place needs no ordering
+// between lanes.  The cos/sin and weight values of a
 // lane's dims stay in registers over up to kHeads heads of one token, whose
 // loads are all in flight together.  4096 tokens x 36 heads of 128 in bf16 take
-// 20.6 us (3.8 TB/s; instruction issue is what is left), 1021 tokens x 129
+// 19.9 us (3.9 TB/s; instruction issue is what is left), 1021 tokens x 129
 // heads of 192 in fp32 36.6 us (5.5 TB/s), eight tokens 2.7 us.
 #include "sa_device.cuh"
 #include "sa_internal.h"
@@ -50,6 +51,12 @@ __device__ __forceinline__ void store_piece(float* p, const float (&v)[4]) {
 }
 __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const float (&v)[4]) {
     *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+}
+// Times a power of two.
+__device__ __forceinline__ void scale_piece(float4& p, float f) { p.x *= f, p.y *= f, p.z *= f, p.w *= f; }
+__device__ __forceinline__ void scale_piece(uint2& p, float f) {
+    const uint32_t f2 = pack_bf16x2(f, f);
+    p.x = hmul2_bf16(p.x, f2), p.y = hmul2_bf16(p.y, f2);
 }
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -125,6 +132,26 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
 #pragma unroll
         for (int i = 0; i < kHeads; ++i) r[i] += __shfl_xor_sync(0xffffffffu, r[i], o);
     const float inv = 1.f / static_cast<float>(a.D);
+    bool outside = false;
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) outside |= norm_factor(r[i] * inv, a.eps) != 1.f;
+    if (__builtin_expect(a.norm && __any_sync(0xffffffffu, outside && n > 0), 0)) {
+        // some head's sum of squares left fp32's range: scaled, and summed again
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) {
+            const float f = norm_factor(r[i] * inv, a.eps);
+            scale_piece(pa[i], f), scale_piece(pb[i], f);
+            float va[4], vb[4], sum = 0.f;
+            unpack(pa[i], va), unpack(pb[i], vb);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += va[j] * va[j] + vb[j] * vb[j];
+            for (int o = 1 << lg_group >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            r[i] = rsqrtf(sum * inv + a.eps * f * f);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kHeads; ++i) r[i] = a.norm ? rsqrtf(r[i] * inv + a.eps) : 1.f;
+    }
     const int64_t ohs = is_k ? a.ko_hs : a.qo_hs;
     T* y = static_cast<T*>(is_k ? a.k_out : a.q_out) + token * (is_k ? a.ko_ts : a.qo_ts) + h0 * ohs + da;
 #pragma unroll
@@ -132,9 +159,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
         if (i >= n) break;
         float va[4], vb[4];
         unpack(pa[i], va), unpack(pb[i], vb);
-        const float ri = a.norm ? rsqrtf(r[i] * inv + a.eps) : 1.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) va[j] *= ri * wa[j], vb[j] *= ri * wb[j];
+        for (int j = 0; j < 4; ++j) va[j] *= r[i] * wa[j], vb[j] *= r[i] * wb[j];
         if (rot) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -183,7 +209,14 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const NormRopeA
     float r = 1.f;
     if (a.norm) {
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        r = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
+        const float f = norm_factor(ss / static_cast<float>(a.D), a.eps);
+        if (__builtin_expect(f != 1.f, 0)) {  // (of the whole warp alike)
+            ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < kMost; ++i) v[i] *= f, u[i] *= f, ss += v[i] * v[i];
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        }
+        r = rsqrtf(ss / static_cast<float>(a.D) + a.eps * f * f);
     }
     const int64_t row = a.rot ? table_row(a, a.positions[token]) * half : 0;
 #pragma unroll
@@ -207,7 +240,7 @@ sa_status launch(const NormRopeArgs& a, cudaStream_t st) {
     auto al = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & (sizeof(T) * kVec - 1)) == 0; };
     auto al16 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
     constexpr int kMany = 4;
-        const int64_t strides = a.q_ts | a.q_hs | a.qo_ts | a.qo_hs | (a.Hk ? a.k_ts | a.k_hs | a.ko_ts | a.ko_hs : 0);
+    const int64_t strides = a.q_ts | a.q_hs | a.qo_ts | a.qo_hs | (a.Hk ? a.k_ts | a.k_hs | a.ko_ts | a.ko_hs : 0);
     // pieces of four dims never straddle a border of the rotated range or of its halves, and pair up
     const bool whole = a.D % 8 == 0 && a.D <= 256 && a.rot % 8 == 0 && a.start % 4 == 0;
     const bool vec = whole && strides % kVec == 0 && al(a.q) && al(a.q_out) && al16(a.q_weight) && al16(a.k_weight) &&
@@ -225,7 +258,7 @@ sa_status launch(const NormRopeArgs& a, cudaStream_t st) {
         return static_cast<unsigned>(((items << lg_group) + kThreads - 1) / kThreads);
     };
     // Four heads per group once that still gives every SM a block: 4096 tokens
-    // x 36 heads of 128 in bf16 take 20.6 us (one head: 32, two: 24.6, eight:
+    // x 36 heads of 128 in bf16 take 19.9 us (one head: 32, two: 24.6, eight:
     // 23.4), 256 tokens 3.5 us (one head: 4.1).
     const bool many = blocks(kMany) >= static_cast<unsigned>(sm_count());
     auto go = [&](auto kernel) { kernel<<<blocks(many ? kMany : 1), kThreads, 0, st>>>(a, lg_group, lanes); };

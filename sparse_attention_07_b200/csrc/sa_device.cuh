@@ -524,6 +524,16 @@ __device__ __forceinline__ void named_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// ---------------------------------------------------------------- RMS norm
+// The factor f that brings a row's values to where fp32 holds their squares, when
+// the mean of those overflowed (finite values from 2^59 on can) or, with an eps
+// too small to hide it, is below 2^-90; else 1.  With the mean m of the scaled
+// values' squares: x * rsqrt(mean(x^2) + eps) = (x f) * rsqrt(m + eps f^2).  (A
+// factor of 2^-70 takes bits only from results below 2^-115.)
+__device__ __forceinline__ float norm_factor(float mean, float eps) {
+    return mean > 3.402823466e38f ? 0x1p-70f : mean + eps < 0x1p-90f ? 0x1p96f : 1.f;
+}
+
 // ---------------------------------------------------------------- quantised latent rows
 // A scale byte e stands for 2^(e-127); 255 marks a block that held a
 // non-finite value and reads as NaN.  The scale as two packed bf16: the byte
