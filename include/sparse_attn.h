@@ -556,8 +556,10 @@ sa_status sa_mla_cache_write(const void* c, int64_t c_in_ld, const void* kr, int
  * Rows of the latent cache by position: c_out [rows][k][512] and kr_out
  * [rows][k][64] (may be NULL), bf16, hold the cached rows of positions idx
  * [rows][k] of sequence seq_of_row[r]; -1 gives zeros.  A quantised value is
- * code * 2^(e-127), which bf16 holds exactly, so this reads back what the
- * attention calls over the cache see.  A position past the page table, or on a
+ * code * 2^(e-127) (e = 0 too, which the write call never stores), which bf16
+ * holds exactly down to its smallest step 2^-133 (bytes below 3 reach below it:
+ * rounded once, to even), so this reads back what the attention calls over the
+ * cache see.  A position past the page table, or on a
  * page outside the pool, records code 0x700 and reads row 0 of the pool.  Layout
  * and alignment of the cache as in sa_mla_cache_write; outputs 16 bytes.
  */

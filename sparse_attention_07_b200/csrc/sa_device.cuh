@@ -537,9 +537,10 @@ __device__ __forceinline__ float norm_factor(float mean, float eps) {
 // ---------------------------------------------------------------- quantised latent rows
 // A scale byte e stands for 2^(e-127); 255 marks a block that held a
 // non-finite value and reads as NaN.  The scale as two packed bf16: the byte
-// is the exponent field (e = 0 is never written; it reads as scale 0).
+// is the exponent field; e = 0, which the write call never stores, is the
+// subnormal 2^-127.
 __device__ __forceinline__ uint32_t q8_scale_bf16x2(uint32_t e) {
-    const uint32_t b = e == 255u ? 0x7FC0u : e << 7;
+    const uint32_t b = e == 255u ? 0x7FC0u : e == 0u ? 0x0040u : e << 7;
     return b | (b << 16);
 }
 
