@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import sparse_attention_07_b200 as sa
-from _latent import D_C, D_R, SCALE, gen, latent64, make_cache, pool_rows
+from _latent import D_C, D_R, SCALE, attend64, gen, latent64, make_cache, pool_rows
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -39,3 +39,27 @@ def test_read_and_attention_agree_on_the_smallest_bytes(kind):
                                page_table=cache["page_table"], seq_of_row=torch.zeros(n, dtype=torch.int32, device=DEV),
                                c_scale=scale)
     assert torch.equal(out.double(), want[:, None].expand(n, 16, D_C))
+
+
+@pytest.mark.parametrize("low,high", [(8, 12), (1, 4), (40, 44)])
+def test_attention_at_the_smallest_scale_bytes(low, high):
+    """Values around 2^-115 (and 2^-122, 2^-83).  The bound is that of the other
+    attention tests, with nothing absolute but the formats' own steps: half a step of
+    bf16's subnormals (2^-134) per value, and fp32's smallest step for each of the
+    n products and their sum.  So an output halved, doubled or zeroed fails."""
+    n = 200
+    cache = make_cache((n,), True, 4, DEV)
+    g = gen(low, DEV)
+    cache["c_scale"].copy_(torch.randint(low, high, cache["c_scale"].shape, generator=g, device=DEV))
+    q = torch.randn(1, 128, D_C, generator=g, device=DEV).bfloat16()
+    qr = torch.randn(1, 128, D_R, generator=g, device=DEV).bfloat16()
+    out = sa.sparse_mla_decode(q, qr, cache["c_cache"], cache["kr_cache"], dev(np.arange(n))[None], SCALE, cache["pps"],
+                               page_table=cache["page_table"], c_scale=cache["c_scale"])
+    want, _, spread, mass = attend64(q[0], qr[0], cache, 0, np.arange(n))
+    slack = 2.0 ** -134 + n * 2.0 ** -149
+    assert slack < 2.0 ** -6 * want.square().mean().sqrt()
+    bound = (2.0 ** -7 + 2.0 ** -16 * mass) * spread + slack
+    err = (out[0].double() - want).abs()
+    assert (err <= bound).all()
+    for wrong in (0.0, 0.5, 2.0):  # such an output would be seen
+        assert ((out[0].double() * wrong - want).abs() > bound).float().mean() > 0.5
