@@ -279,7 +279,8 @@ def sparse_mla_prefill_workspace_size(rows: int, H: int, k: int, d_c: int = 512)
 
 def sparse_mla_prefill(q_lat, q_rope, c_cache, kr_cache, idx, scale: float, pages_per_seq: int, page_table=None,
                        seq_of_row=None, out=None, lse=None, workspace=None, c_scale=None):
-    """sparse_mla_decode for many rows (one key split per row)."""
+    """sparse_mla_decode for many rows: one key split per row, but with `c_scale`
+    as many as sparse_mla_decode takes (workspace: sparse_mla_q8_workspace_size)."""
     if c_scale is not None:
         return _sparse_mla_q8(q_lat, q_rope, c_cache, c_scale, kr_cache, idx, scale, pages_per_seq, page_table,
                               seq_of_row, out, lse, workspace)
@@ -477,7 +478,8 @@ def _need(t, name: str, dtypes, shape=None, contiguous=True):
     raise ValueError(f"{name} must be contiguous")
 
 
-_SCALE_TYPES = (torch.uint8, torch.float8_e8m0fnu)
+# (torch before 2.7 has no float8_e8m0fnu)
+_SCALE_TYPES = (torch.uint8,) + ((torch.float8_e8m0fnu,) if hasattr(torch, "float8_e8m0fnu") else ())
 _POOL_TYPES = (torch.float8_e4m3fn, torch.bfloat16)
 _IO_TYPES = (torch.bfloat16, torch.float32)
 _F32, _BF16, _I32 = (torch.float32,), (torch.bfloat16,), (torch.int32,)
