@@ -112,8 +112,9 @@ sa_status sa_check_device_error(int* code_out, sa_stream_t stream);
  * Sets, for the current GPU, the time limit of the kernels' waits on other
  * parties (a ring slot filled by another warp, a partner CTA's signal), in
  * nanoseconds; 0 restores the default of one second.  Waits of a CTA for its
- * own copies and tensor-core work in flight before it exits always keep the
- * one-second limit, so a kernel whose wait ran out still drains its own work
+ * own copies and tensor-core work in flight before it exits always keep a
+ * limit of one second (three in the CTA of a latent-cache attention pair whose
+ * partner issues the products), so a kernel whose wait ran out still drains its own work
  * and frees its tensor memory before it returns.  A short limit makes a
  * kernel give up (and record its site code) instead of waiting: a way to
  * exercise the failure path.  A limit above what a kernel can time counts as

@@ -48,8 +48,6 @@
 // of 128 registers 87 us; a second tile of rows in flight per warp, as copies or
 // as a doubled loop, 79 to 83; loading warps taking turns with double the rows 70),
 // softmax groups that alternate tiles and issuing products by readiness the same.
-#include <algorithm>
-
 #include "sa_device.cuh"
 #include "sa_internal.h"
 #include "sa_wait.h"
@@ -700,12 +698,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             if (elect_one()) tc_commit_pair(&bar_final);
             __syncwarp();
         }
-        // every product has finished (fixed limit), and the last arrival this CTA gets has come, before
-        // the pair tears down (the even CTA's waits all have limits)
-        if (lane == 0) {
-            if (!Waits::own(&bar_final, 0, static_cast<uint32_t>(rank ? 3 * kWaitLimitNs : kWaitLimitNs))) s_abort = 12;
-        }
-        __syncwarp();
     }
     if (warp < kSmxWarps) {
         // ---------------------------------------------- softmax + output
@@ -933,7 +925,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 
     tc_fence_before();
     __syncthreads();
-    if (tid == 0 && *wait.abort) record_error(a.err, kErrLatWait | *wait.abort);
+    if (warp == kMmaWarp) {
+        // Every product has finished, and the last arrival this CTA gets has come, before the pair tears down.  The
+        // roles have ended, so what is left is work in flight (fixed limit), and for the odd CTA the even one's way
+        // to its last commit, which a wait of the even one's may hold up (kMaxWait32Ns at most).
+        if (lane == 0) {
+            if (nt > 0 && !Waits::own(&bar_final, 0, static_cast<uint32_t>(rank ? 3 * kWaitLimitNs : kWaitLimitNs))) s_abort = 12;
+            if (*wait.abort) record_error(a.err, kErrLatWait | *wait.abort);
+        }
+        __syncwarp();
+    }
     cluster_sync_all();  // no more remote arrivals, stores or products in either CTA
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
@@ -1056,9 +1057,7 @@ sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cuda
     // 25 / 37 / 49 against 27 / 38 / 48.
     if (a.idx && ka.nsplit == 1) {
         const int64_t pairs = sm_count() / 2, tiles = (a.k + kNK - 1) / kNK;
-        // (the end of a pair's work is waited for with a limit: some 4000 items, 60 ms, a pair at most)
-        if (items > pairs && (tiles <= 4 || (tiles <= 8 && items > 2 * pairs)))
-            ka.stride = static_cast<int>(std::max(pairs, (items + 4095) / 4096));
+        if (items > pairs && (tiles <= 4 || (tiles <= 8 && items > 2 * pairs))) ka.stride = static_cast<int>(pairs);
     }
     if (ka.nsplit > 1) {
         if (!ws || ws_bytes < state_bytes(items, ka.nsplit)) return SA_EINVAL;
