@@ -136,6 +136,7 @@ struct Waits {
     }
     // (one lane) Without the abort word: for a role's own work in flight.
     __device__ __forceinline__ static bool own(uint64_t* b, uint32_t parity, uint32_t limit_ns) {
+        if (mbar_try_wait(b, parity)) return true;
         const uint32_t t0 = now();
 #pragma unroll 1
         while (!mbar_try_wait(b, parity))
@@ -301,9 +302,9 @@ __device__ __forceinline__ bool bad4(uint4 v) {
 }
 
 // A 16-byte piece of a drafted row's operand, of the aggregation (v) or of the scores.
-__device__ __forceinline__ void clean_piece(uint32_t at, bool v) {
+__device__ __forceinline__ void clean_piece(uint32_t at, uint4 piece, bool v) {
     const uint32_t w = v ? 0u : 0x7FC07FC0u;
-    if (bad4(ld_smem_v4(at))) st_smem_v4(at, make_uint4(w, w, w, w));
+    if (bad4(piece)) st_smem_v4(at, make_uint4(w, w, w, w));
 }
 
 // An item's query rows (its first is row q0 of the queries, `rows` of them this CTA's) by warp w
@@ -608,8 +609,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 #pragma unroll 1
                     for (int i = max(0, s_it.past - (s_t0 + t) * kNK - row0); i < 4; ++i) {
                         const uint32_t dst = (at + i * 128) ^ (i << 4);
-                        clean_piece(dst, v);
-                        clean_piece(dst ^ 16, v);
+                        clean_piece(dst, ld_smem_v4(dst), v);
+                        clean_piece(dst ^ 16, ld_smem_v4(dst ^ 16), v);
                     }
                 }
                 __syncwarp();
@@ -626,12 +627,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             const int st = t & 1;
             if (!wait(&landed[st], static_cast<uint32_t>(t >> 1 & 1), 13)) break;
             const int pos0 = (t0 + t) * kNK + (v ? 0 : own0);  // of the operand's row 0
-            if ((t0 + t + 1) * kNK > it.past) {  // lane = 16-byte pieces of a row
+            if ((t0 + t + 1) * kNK > it.past) {  // 16-byte pieces, row after row
                 const uint32_t at0 = v ? vbase + st * kVStage : kbase + st * 8 * kKSlice, slice = v ? kVSlice : kKSlice;
                 const int rows = v ? kNK : min(kOwn, it.n_keys - pos0);  // (scores of keys past the last are masked)
-                for (int j = max(0, it.past - pos0); j < rows; ++j)
-                    for (int p = lane; p < (v ? 32 : 64); p += 32)
-                        clean_piece(at0 + (p >> 3) * slice + j * 128 + (((p & 7) ^ (j & 7)) << 4), v);
+                const int lg = v ? 5 : 6;
+#pragma unroll 1
+                for (int q0 = max(0, it.past - pos0) << lg; q0 < rows * (1 << lg); q0 += 128) {  // four pieces a lane at once
+                    uint32_t at[4];
+                    uint4 w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int q = q0 + 32 * k + lane, j = q >> lg, p = q & ((1 << lg) - 1);
+                        at[k] = at0 + (p >> 3) * slice + j * 128 + (((p & 7) ^ (j & 7)) << 4);
+                        w[k] = j < rows ? ld_smem_v4(at[k]) : make_uint4(0u, 0u, 0u, 0u);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) clean_piece(at[k], w[k], v);
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
             }
