@@ -120,12 +120,18 @@ struct Waits {
         asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
         return t;
     }
+    // kCluster: for reports of operands from both CTAs of the pair (mbar_arrive_remote).
+    template <bool kCluster>
+    __device__ __forceinline__ static bool poll(uint64_t* b, uint32_t parity) {
+        return kCluster ? mbar_try_wait_acq_cluster(b, parity) : mbar_try_wait(b, parity);
+    }
     // (one lane)
+    template <bool kCluster = false>
     __device__ __forceinline__ bool one(uint64_t* b, uint32_t parity, int site) const {
-        if (mbar_try_wait(b, parity)) return true;
+        if (poll<kCluster>(b, parity)) return true;
         const uint32_t t0 = now();
 #pragma unroll 1
-        while (!mbar_try_wait(b, parity)) {
+        while (!poll<kCluster>(b, parity)) {
             if (*abort) return false;
             if (wait32_over(t0, now(), limit_ns)) {
                 *abort = site;
@@ -144,12 +150,16 @@ struct Waits {
         return true;
     }
     // The whole warp leaves together.
-    __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity, int site) const {
-        if (__all_sync(0xffffffffu, mbar_try_wait(b, parity))) return true;
+    template <bool kCluster = false>
+    __device__ __forceinline__ bool warp(uint64_t* b, uint32_t parity, int site) const {
+        if (__all_sync(0xffffffffu, poll<kCluster>(b, parity))) return true;
         int ok = 1;
-        if ((threadIdx.x & 31) == 0) ok = one(b, parity, site) ? 1 : 0;
+        if ((threadIdx.x & 31) == 0) ok = one<kCluster>(b, parity, site) ? 1 : 0;
         return __shfl_sync(0xffffffffu, ok, 0) != 0;
     }
+    __device__ __forceinline__ bool operator()(uint64_t* b, uint32_t parity, int site) const { return warp(b, parity, site); }
+    // For operands reported by both CTAs of the pair.
+    __device__ __forceinline__ bool pair(uint64_t* b, uint32_t parity, int site) const { return warp<true>(b, parity, site); }
 };
 
 // What one item covers.
@@ -664,12 +674,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
 #pragma unroll 1
             for (int n = 0; ok && n < n_items; ++n, g += nt) {
                 // the next item's query is in place
-                if (n > 0 && !wait(&bar_query, static_cast<uint32_t>(n & 1) ^ 1, 3)) break;
+                if (n > 0 && !wait.pair(&bar_query, static_cast<uint32_t>(n & 1) ^ 1, 3)) break;
 #pragma unroll 1
                 for (int u = 0; u <= nt; ++u) {
                     if (u < nt) {  // scores(u)
                         const int t = g + u, sb = t & 1;
-                        ok = wait(&bar_kfull[sb], static_cast<uint32_t>(t >> 1 & 1), 3) &&
+                        ok = wait.pair(&bar_kfull[sb], static_cast<uint32_t>(t >> 1 & 1), 3) &&
                              (t < 2 || wait(&bar_sfree[sb], static_cast<uint32_t>(t >> 1 & 1) ^ 1, 4));
                         if (!ok) break;
                         tc_fence_after();
@@ -689,8 +699,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                     }
                     if (u > 0) {  // aggregation(u - 1)
                         const int t = g + u - 1, st = t & 1;
-                        ok = wait(&bar_vfull[st], static_cast<uint32_t>(t >> 1 & 1), 5) &&
-                             wait(&bar_pfull, static_cast<uint32_t>(t & 1), 6) &&
+                        ok = wait.pair(&bar_vfull[st], static_cast<uint32_t>(t >> 1 & 1), 5) &&
+                             wait.pair(&bar_pfull, static_cast<uint32_t>(t & 1), 6) &&
                              (u > 1 || n == 0 || wait(&bar_ofree, static_cast<uint32_t>(n & 1) ^ 1, 6));
                         if (!ok) break;
                         tc_fence_after();

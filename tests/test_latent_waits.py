@@ -53,3 +53,23 @@ def test_the_kernel_uses_the_checked_limit():
         source = f.read()
     assert "wait32_limit(wait_limit_of(" in source
     assert "wait_limit_of(" not in source.replace("wait32_limit(wait_limit_of(", "")
+
+
+def test_reports_between_the_ctas_of_a_pair_order_their_operands():
+    """The thread that issues a pair's products reads operands of both CTAs: reports release, and its waits
+    acquire, at cluster scope (a release at CTA scope would order them for the writing CTA's threads only)."""
+    with open(os.path.join(CSRC, "sa_device.cuh")) as f:
+        device = f.read()
+
+    def body(name):
+        start = device.index(f" {name}(")
+        return device[start:device.index("\n}", start)]
+
+    arrive = body("mbar_arrive_remote")
+    assert "fence.release.sync_restrict::shared::cta.cluster" in arrive or "arrive.release.cluster" in arrive
+    assert ".cta;" not in arrive.replace("shared::cta.cluster;", "")
+    assert "try_wait.parity.acquire.cluster" in body("mbar_try_wait_acq_cluster")
+    with open(os.path.join(CSRC, "mla_latent.cu")) as f:
+        source = f.read()
+    for bar in ("bar_kfull", "bar_vfull", "bar_pfull", "bar_query"):
+        assert f"wait.pair(&{bar}" in source and f"wait(&{bar}" not in source, bar
