@@ -578,7 +578,11 @@ sa_status sa_mla_cache_read(const void* c_cache, sa_dtype cache_dtype, int64_t c
  * enters both products with the exact value code * 2^(e-127) (codes 0x7F and
  * 0xFF, which the write call never stores, are not valid contents).  out is fp32
  * (SA_F32) or bf16 (SA_BF16: rounded once).  sa_dense_mla_q8 attends to positions
- * 0 .. n_visible[r]-1 instead of a selection.  The workspace (256-byte aligned,
+ * 0 .. n_visible[r]-1 instead of a selection, L_max >= n_visible[r] for every r.
+ * The tensor cores' fp32 sums fall short by n 2^-27 of a sum of n keys of one sign;
+ * k or L_max above 2^18 splits a row so that n is 2^18 at most (2e-3), or 1/32 of
+ * the row from 2^23 keys on.  A row longer than L_max is attended to whole, in the
+ * splits of L_max.  The workspace (256-byte aligned,
  * scratch) may be NULL when its size is 0; concurrent calls need separate ones.
  */
 size_t sa_sparse_mla_q8_workspace_size(int rows, int H, int k);
@@ -614,7 +618,8 @@ sa_status sa_dense_mla_q8(const void* q_lat, const void* q_rope, const void* c_c
  *   infinite contents included; a token that sees a drafted row with a NaN or an
  *   infinity among its latent values gets NaN in its output and lse.
  *   L_max >= n_past[b] + n_draft[b] for every b sets the key split and the
- *   workspace; a longer sequence still gives right results.
+ *   workspace; a longer sequence is attended to whole (long sums: see
+ *   sa_sparse_mla_q8).
  * cache_dtype SA_BF16 (c_scale NULL, c_ld in elements) or SA_E4M3.
  * 1 <= T <= SA_TREE_MAX_TOKENS, H <= 128.  Workspace as sa_sparse_mla_q8.
  */

@@ -1022,12 +1022,18 @@ int tokens_per_item(int T, int H) {
 }
 
 // Key splits of an item: as many as fill the GPU's CTA pairs, each of at least
-// three tiles.
+// three tiles, and so many that none is longer than 2^18 keys (as far as 32 splits
+// go): the tensor cores cut off what of a product lies below 2^-25 of the sum it is
+// added to, so the output of n keys of the same sign falls short by n 2^-27
+// (measured, one split: 2e-3 at 2^18, 8e-3 at 2^20, 3.3e-2 at 2^22; 16 splits of
+// the last 2e-3).
+constexpr int kLongTiles = (1 << 18) / kNK;
 int splits(int64_t items, int k) {
     const int64_t pairs = sm_count() / 2;
     const int tiles = (k + kNK - 1) / kNK;
     int64_t ns = items >= pairs ? 1 : pairs / items;
     if (ns > tiles / 3) ns = tiles / 3;
+    if (ns < (tiles + kLongTiles - 1) / kLongTiles) ns = (tiles + kLongTiles - 1) / kLongTiles;
     if (ns > kMaxSplits) ns = kMaxSplits;
     return ns < 1 ? 1 : static_cast<int>(ns);
 }
