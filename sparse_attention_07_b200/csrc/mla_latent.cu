@@ -25,7 +25,10 @@
 //    softmax; the four threads of a row exchange tile maxima through shared
 //    memory, O is rescaled only when a maximum grows by more than 2^8.  P goes
 //    to shared memory as bf16, as the tensor cores take it (half a step, 2^-8, of
-//    each weight); normaliser and lse use the fp32 values.
+//    each weight); the normaliser is the sum of the weights as rounded, so that
+//    the weights applied sum to 1, and the lse uses the fp32 values.  (Two sums cost
+//    5 us of 1024 x 2048 rows; with one, 2^15 keys of one sign were off by 5e-4,
+//    with two by 2e-4.)
 //  * One thread of the even CTA issues scores(t + 1) before aggregation(t).
 //  * Drafted rows are masked token by token, so a row that some token must not see
 //    may be in the tile; non-finite contents of such a row are zeroed in the
@@ -379,7 +382,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     // the next item's query is in place, the last one's output is read (the even CTA's copies)
     __shared__ uint64_t bar_query, bar_ofree;
     __shared__ float s_max[2][32 * kSmxWarps];
-    __shared__ float s_sum[32 * kSmxWarps];
+    __shared__ float s_sum[2][32 * kSmxWarps];  // of a thread's weights, and of them as rounded
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     __shared__ Item s_it;  // (drafted tokens' masks read it: no registers for it in the loops)
@@ -778,7 +781,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
         int t = 0;  // of the pair's tiles
 #pragma unroll 1
         for (int n = 0; n < n_items; ++n) {
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f, lr = 0.f;  // lr: the sum of the rounded weights
             bool failed = false;
 #pragma unroll 1
             for (int u = 0; u < nt; ++u, ++t) {
@@ -838,18 +841,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                         }
                     }
                     l *= alpha;
+                    lr *= alpha;
                     m = m_new;
                 }
                 const float mref = m == -INFINITY ? 0.f : m;  // masked keys are -inf and give exactly 0
                 uint32_t pk[8];
-                float sum = 0.f;
+                float sum = 0.f, sumr = 0.f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     const float p0 = fast_exp2(s[2 * j] * c2 - mref), p1 = fast_exp2(s[2 * j + 1] * c2 - mref);
                     sum += p0 + p1;
                     pk[j] = pack_bf16x2(p0, p1);
+                    sumr += __uint_as_float(pk[j] << 16) + __uint_as_float(pk[j] & 0xFFFF0000u);
                 }
                 l += sum;
+                lr += sumr;
                 // aggregation(t - 1) has read P
                 if (ok && t > 0)
                     ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 10);
@@ -865,9 +871,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 }
             }
             // ---- the row's sums, then the rows out: staged over the idle operands, bulk copies
-            s_sum[tid] = l;
+            s_sum[0][tid] = l;
+            s_sum[1][tid] = lr;
             named_sync(1, 32 * kSmxWarps);
-            l = (s_sum[r] + s_sum[r + 64]) + (s_sum[r + 128] + s_sum[r + 192]);  // (one order in all four)
+            l = (s_sum[0][r] + s_sum[0][r + 64]) + (s_sum[0][r + 128] + s_sum[0][r + 192]);  // (one order in all four)
+            lr = (s_sum[1][r] + s_sum[1][r + 64]) + (s_sum[1][r + 128] + s_sum[1][r + 192]);
             const int m_row = static_cast<int>(cluster_rank()) * kRows + r;
             const bool live = m_row < s_it.tokens * a.H;
             const int64_t orow = (static_cast<int64_t>(s_it.b + n * ka.stride) * a.T + s_it.i0) * a.H + m_row;
@@ -880,7 +888,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 const bool partial = ka.nsplit > 1;
                 const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
                 const bool empty = l == 0.f;  // (a NaN sum is not empty)
-                const float inv = empty || partial ? 1.f : 1.f / l;
+                // divided by the rounded weights' sum; a split's share of the row is that of its weights
+                const float inv = empty ? 1.f : (partial ? l : 1.f) / lr;
                 const bool bf = !partial && a.out_bf16 != nullptr;
                 dst = partial ? reinterpret_cast<uint8_t*>(ka.ws_o + wrow * 512)
                               : (bf ? static_cast<uint8_t*>(a.out_bf16) + orow * 1024 : reinterpret_cast<uint8_t*>(a.out + orow * 512));
