@@ -209,14 +209,17 @@ __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const NormRopeA
     float r = 1.f;
     if (a.norm) {
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float f = norm_factor(ss / static_cast<float>(a.D), a.eps);
+        float mean = ss / static_cast<float>(a.D), eps = a.eps;
+        const float f = norm_factor(mean, eps);
         if (__builtin_expect(f != 1.f, 0)) {  // (of the whole warp alike)
             ss = 0.f;
 #pragma unroll
             for (int i = 0; i < kMost; ++i) v[i] *= f, u[i] *= f, ss += v[i] * v[i];
             for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            mean = ss / static_cast<float>(a.D);
+            eps = eps * f * f;
         }
-        r = rsqrtf(ss / static_cast<float>(a.D) + a.eps * f * f);
+        r = rsqrtf(mean + eps);
     }
     const int64_t row = a.rot ? table_row(a, a.positions[token]) * half : 0;
 #pragma unroll
