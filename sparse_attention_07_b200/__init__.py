@@ -586,7 +586,8 @@ def mla_cache_write(c, kr, c_cache, kr_cache, slots, pages_per_seq: int, cos, si
     byte per 128 dims when c_scale ([rows, 4] uint8 or float8_e8m0fnu) is
     given; kr [tokens, 64] rotated by row positions[t] (None: slots[t]) of
     cos and sin [n_pos, 32].  slots [tokens] int32: position of the token in
-    sequence seq_of_row[t] (None: t), -1: skip the token."""
+    sequence seq_of_row[t] (None: t), -1: skip the token; two tokens of one
+    call must not name the same row.  Without `norm` a weight still applies."""
     tokens = c.shape[0]
     _need(c, "c", _IO_TYPES, (tokens, 512), False)
     _need(kr, "kr", (c.dtype,), (tokens, 64), False)

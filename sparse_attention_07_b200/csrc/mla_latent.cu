@@ -42,11 +42,12 @@
 //    item's scores are done, and its output leaves straight from tensor memory while
 //    the next item's tiles are under way.
 //
-// Measured: 1024 queries x 2048 selected e4m3 rows x 128 heads in 0.88 ms (665
-// TFLOP/s), 74 of them (one per pair) in 63 us: 1.55 us per tile and 14 us around
-// them.  The tensor cores are at work for 30 percent of that.  What is left is the
-// hand-over from role to role: with conversion, row loads and seven eighths of the
-// products left out a tile still takes 1.36 us.  So the warps are many (28, of 72
+// Measured (device time, replayed graph): 1024 queries x 2048 selected e4m3 rows x
+// 128 heads in 0.89 ms (656 TFLOP/s), 74 of them (one per pair) in 64 us: 1.56 us
+// per tile and 14 us around them.  The tensor cores are at work for 30 percent of
+// that.  What is left is the hand-over from role to role: an earlier version, of
+// 63.6 us, still took 54.4 with conversion, row loads, seven eighths of the products
+// and the exponentials left out.  So the warps are many (28, of 72
 // registers) and their loops short: fewer or longer ones ran slower (sixteen warps
 // of 128 registers 87 us; a second tile of rows in flight per warp, as copies or
 // as a doubled loop, 79 to 83; loading warps taking turns with double the rows 70),
@@ -111,9 +112,9 @@ struct Args {
     float* ws_ml;  // [item][nsplit][128][2]: m, l
 };
 
-// Waits of this kernel.  The code is small (some thirty of them are inlined, and
-// the roles' loops together have to stay in the instruction cache): a wait that
-// runs out leaves its site in the CTA's abort word, and the CTA's end records it.
+// Waits of this kernel.  Their code is small, since some thirty of them are inlined
+// in the roles' loops: a wait that runs out leaves its site in the CTA's abort word,
+// and the CTA's end records it.
 struct Waits {
     volatile int* abort;
     uint32_t limit_ns;
@@ -1089,7 +1090,7 @@ sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cuda
     ka.items = static_cast<int>(items);
     // Short selections, more of them than pairs, go to the pairs in turn (equal tiles each), so that an item's
     // query and first rows load behind the output before: 500 rows x 128 heads of 64 / 256 / 512 slots take
-    // 78 / 115 / 170 us against 100 / 137 / 184 with a pair for each, 768 the same, 1024 285 against 273 (a tile
+    // 79 / 115 / 171 us against 100 / 137 / 184 with a pair for each, 768 the same, 1024 285 against 273 (a tile
     // takes 2.0 us there against 1.56: the loops around the tiles' cost registers); 100 rows of 64 / 200 / 400
     // 25 / 37 / 49 against 27 / 38 / 48.
     if (a.idx && ka.nsplit == 1) {

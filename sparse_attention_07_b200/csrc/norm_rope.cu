@@ -15,8 +15,8 @@
 // between lanes.  The cos/sin and weight values of a
 // lane's dims stay in registers over up to kHeads heads of one token, whose
 // loads are all in flight together.  4096 tokens x 36 heads of 128 in bf16 take
-// 19.9 us (3.9 TB/s; instruction issue is what is left), 1021 tokens x 129
-// heads of 192 in fp32 36.6 us (5.5 TB/s), eight tokens 2.7 us.
+// 19.9 us (3.9 TB/s; issue slots 69 percent busy), 1021 tokens x 129
+// heads of 192 in fp32 36.7 us (5.5 TB/s), eight tokens 2.7 us.
 #include "sa_device.cuh"
 #include "sa_internal.h"
 
@@ -177,8 +177,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_kernel(const NormRopeArgs 
 }
 
 // Any D up to 512, any strides and alignment: one warp per head, lane owns
-// dims lane, lane + 32, ...  (4096 tokens x 36 heads of 120 in bf16 take 114 us
-// here and 21 us above.)
+// dims lane, lane + 32, ...  (4096 tokens x 36 heads in bf16: 116 us for 124 dims,
+// 121 for 128 at odd addresses; 120 dims 20 us above.)
 template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_rope_any_kernel(const NormRopeArgs a) {
     constexpr int kMost = 16;

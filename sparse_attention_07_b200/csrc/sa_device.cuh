@@ -380,10 +380,9 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t adesc, u
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// True in one lane of a converged warp.  MMAs issued under it from a
-// warp-uniform loop keep their descriptors in uniform registers: a run of
-// M = 128, N = 64 pair products issues every 25 cycles, against 48 from code
-// that only one lane reaches.
+// True in one lane of a converged warp.  A run of M = 128, N = 64 pair products
+// issued under it from a warp-uniform loop takes 25 cycles each, against 48 from
+// code that only one lane reaches.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -566,7 +565,6 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w, uint32_t scale2) {
     const uint32_t h = ((hi >> 4) & 0x07F007F0u) | (hi & 0x80008000u);
     return make_uint2(hmul2_bf16(hmul2_bf16(l, k2p120), scale2), hmul2_bf16(hmul2_bf16(h, k2p120), scale2));
 }
-
 
 // Four e4m3 codes -> four bf16 in the order 0, 2, 1, 3 (codes 1 and 3 already
 // stand in the upper bytes of the two halves, which saves shifts), times a factor
