@@ -580,6 +580,7 @@ sa_status sa_mla_cache_read(const void* c_cache, sa_dtype cache_dtype, int64_t c
  * (SA_F32) or bf16 (SA_BF16: rounded once).  sa_dense_mla_q8 attends to positions
  * 0 .. n_visible[r]-1 instead of a selection, L_max >= n_visible[r] for every r.
  * The tensor cores' fp32 sums fall short by n 2^-27 of a sum of n keys of one sign;
+ * k, L_max and the positions of a page table are 2^30 at most.
  * k or L_max above 2^18 splits a row so that n is 2^18 at most (2e-3), or 1/32 of
  * the row from 2^23 keys on.  A row longer than L_max is attended to whole, in the
  * splits of L_max.  The workspace (256-byte aligned,

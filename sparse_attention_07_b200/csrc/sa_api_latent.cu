@@ -177,6 +177,8 @@ static sa_status latent_attn(const void* q_lat, const void* q_rope, const void* 
                                     page_table, pages_per_seq, seq_of_row, d_c, d_R);
     if (s != SA_OK) return s;
     if (H > 128 || T > SA_TREE_MAX_TOKENS || k > kMaxKeys || (out_dtype != SA_F32 && out_dtype != SA_BF16)) return SA_EUNSUPPORTED;
+    // (a length read on the device is cut to the page table and one page, which 32 bits hold)
+    if (pages_per_seq > kMaxKeys / 64) return SA_EUNSUPPORTED;
     if (!q_lat || !q_rope || !out || (!idx && !n_past)) return SA_EINVAL;
     if (!aligned(q_lat, 16) || !aligned(q_rope, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(idx, 4) ||
         !aligned(n_past, 4) || !aligned(n_draft, 4))

@@ -131,3 +131,12 @@ def test_cpu_tensors_are_refused():
     q = torch.zeros(1, 2, 64)
     with pytest.raises(ValueError):
         sa.qk_norm_rope(q, None, None, None, None)
+
+
+def test_page_tables_of_more_positions_than_32_bits_count(L):
+    """A row's keys (up to the table's positions, and drafted ones) are counted in 32 bits."""
+    call = caller(L.sa_dense_mla_q8, ql=FAKE, qr=FAKE, cc=FAKE, cld=512, cs=FAKE, sld=4, krc=FAKE, krld=64, pool=4, pt=FAKE,
+                  pps=2 ** 24 + 1, sor=None, n=FAKE, rows=1, H=128, L_max=64, dc=512, dR=64, scale=0.07, out=FAKE,
+                  odt=sa.SA_F32, lse=None, ws=None, wsb=0, st=None)
+    assert call() == sa.SA_EUNSUPPORTED
+    assert call(pps=2 ** 31 - 1) == sa.SA_EUNSUPPORTED
