@@ -582,7 +582,9 @@ sa_status sa_mla_cache_read(const void* c_cache, sa_dtype cache_dtype, int64_t c
  * The tensor cores' fp32 sums fall short by n 2^-27 of a sum of n keys of one sign;
  * k, L_max and the positions of a page table are 2^30 at most.
  * k or L_max above 2^18 splits a row so that n is 2^18 at most (2e-3), or 1/32 of
- * the row from 2^23 keys on.  A row longer than L_max is attended to whole, in the
+ * the row from 2^23 keys on (rows shorter than 2^18 under a larger L_max are not
+ * split, but the call is some ten percent slower than under a tight one).  A row
+ * longer than L_max is attended to whole, in the
  * splits of L_max.  The workspace (256-byte aligned,
  * scratch) may be NULL when its size is 0; concurrent calls need separate ones.
  */

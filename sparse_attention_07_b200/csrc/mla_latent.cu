@@ -52,6 +52,8 @@
 // of 128 registers 87 us; a second tile of rows in flight per warp, as copies or
 // as a doubled loop, 79 to 83; loading warps taking turns with double the rows 70),
 // softmax groups that alternate tiles and issuing products by readiness the same.
+#include <algorithm>
+
 #include "sa_device.cuh"
 #include "sa_internal.h"
 #include "sa_wait.h"
@@ -95,6 +97,11 @@ constexpr uint32_t kColO = 0;    // two 256-dim products, 128 columns each
 constexpr uint32_t kColS = 256;  // two score buffers of 32 columns
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxSplits = 32;
+// Keys of a split at most (as far as kMaxSplits go): the tensor cores cut off what
+// of a product lies below 2^-25 of the sum it is added to, so the output of n keys
+// of the same sign falls short by n 2^-27 (measured, one split: 2e-3 at 2^18, 8e-3
+// at 2^20, 3.3e-2 at 2^22; 16 splits of the last 2e-3).
+constexpr int kLongKeys = 1 << 18;
 
 // Tensor maps of the bf16 pools: latent rows in boxes of 64 dims by 32 rows (c) and
 // by 64 rows (cv), RoPE keys by 32 rows, 128-byte swizzle.
@@ -106,7 +113,8 @@ struct Args {
     LatentArgs a;
     int tokens_per_item;  // P: tokens of a tree in one item's 128 rows
     int groups;           // items per tree
-    int nsplit;
+    int nsplit;           // key splits at most, and at least (an item's own: Item)
+    int base;
     int items, stride;  // stride > 0 (selections): a pair takes items p, p + stride, ... of them, of equal tiles
     float* ws_o;   // [item][nsplit][128][512]
     float* ws_ml;  // [item][nsplit][128][2]: m, l
@@ -168,7 +176,7 @@ struct Waits {
 
 // What one item covers.
 struct Item {
-    int b, i0, seq, past, nd, n_keys, tokens;
+    int b, i0, seq, past, nd, n_keys, tokens, splits;
 };
 
 __device__ __forceinline__ Item item_of(const Args& ka, int item) {
@@ -182,6 +190,7 @@ __device__ __forceinline__ Item item_of(const Args& ka, int item) {
     it.past = a.idx ? 0 : static_cast<int>(min(static_cast<int64_t>(max(a.n_past[it.b], 0)), a.pages_per_seq * int64_t(kPage) + kPage));
     it.n_keys = a.idx ? a.k : it.past + it.nd;
     it.tokens = min(ka.tokens_per_item, (a.tree ? it.nd : a.T) - it.i0);  // <= 0: nothing to do
+    it.splits = min(max(ka.base, (it.n_keys + kLongKeys - 1) / kLongKeys), ka.nsplit);
     return it;
 }
 
@@ -393,12 +402,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int cl = blockIdx.x >> 1;
-    const int item = cl / ka.nsplit, split = cl % ka.nsplit;
+    const int item = cl % ka.items, split = cl / ka.items;  // (splits that a short row does not have come last)
     const Item it = item_of(ka, item);
-    if (it.tokens <= 0) return;  // both CTAs of the pair alike
+    if (it.tokens <= 0 || split >= it.splits) return;  // both CTAs of the pair alike
     const int tiles = (it.n_keys + kNK - 1) / kNK;
-    const int t0 = static_cast<int>(static_cast<int64_t>(split) * tiles / ka.nsplit);
-    const int nt = static_cast<int>(static_cast<int64_t>(split + 1) * tiles / ka.nsplit) - t0;
+    // (2^24 tiles, and 32 splits, stay below 2^31)
+    const int t0 = split * tiles / it.splits, nt = (split + 1) * tiles / it.splits - t0;
     // the tiles of all of this pair's items are one stream for the roles (stages and barriers go on from
     // item to item): nt of each
     const int n_items = kMany ? (ka.items - item + ka.stride - 1) / ka.stride : 1;
@@ -886,7 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
                 ok = wait(&bar_o[(t - 1) & 1], static_cast<uint32_t>((t - 1) >> 1 & 1), 11);
             if (ok && !*wait.abort) {
                 tc_fence_after();
-                const bool partial = ka.nsplit > 1;
+                const bool partial = s_it.splits > 1;
                 const int64_t wrow = (static_cast<int64_t>(item) * ka.nsplit + split) * 128 + m_row;
                 const bool empty = l == 0.f;  // (a NaN sum is not empty)
                 // divided by the rounded weights' sum; a split's share of the row is that of its weights
@@ -946,7 +955,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) mla_lat
             if (last) {
                 named_sync(1, 32 * kSmxWarps);  // the threads of a row have staged it (one bulk copy per row)
                 if (ok && !*wait.abort && live && tid < kRows) {
-                    bulk_copy_s2g(dst, sm + r * kORow, ka.nsplit == 1 && a.out_bf16 ? 1024 : 2048);
+                    bulk_copy_s2g(dst, sm + r * kORow, s_it.splits == 1 && a.out_bf16 ? 1024 : 2048);
                     bulk_wait_all();
                 }
             } else {
@@ -987,10 +996,12 @@ __global__ void __launch_bounds__(kCombThreads) mla_latent_combine_kernel(const 
     const int b = static_cast<int>(orow / a.H / a.T);
     if (a.tree && a.n_draft && token >= a.n_draft[b]) return;
     const int item = b * ka.groups + token / ka.tokens_per_item;
+    const int splits = item_of(ka, item).splits;
+    if (splits == 1) return;  // (written by its pair)
     const int64_t w0 = static_cast<int64_t>(item) * ka.nsplit * 128 + token % ka.tokens_per_item * a.H + h;
     // lane s holds split s's state
     float ms = -INFINITY, ls = 0.f;
-    if (lane < ka.nsplit) {
+    if (lane < splits) {
         const float2 v = *reinterpret_cast<const float2*>(ka.ws_ml + (w0 + static_cast<int64_t>(lane) * 128) * 2);
         ms = v.x, ls = v.y;
     }
@@ -1003,16 +1014,16 @@ __global__ void __launch_bounds__(kCombThreads) mla_latent_combine_kernel(const 
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     const float4* src = reinterpret_cast<const float4*>(ka.ws_o + w0 * 512) + 32 * p + lane;
-    for (int s0 = 0; s0 < ka.nsplit; s0 += 8) {
+    for (int s0 = 0; s0 < splits; s0 += 8) {
         float4 v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (s0 + i < ka.nsplit) v[i] = src[static_cast<int64_t>(s0 + i) * 128 * 128];
+            if (s0 + i < splits) v[i] = src[static_cast<int64_t>(s0 + i) * 128 * 128];
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float w = __shfl_sync(0xffffffffu, wgt, s0 + i);  // (s0 + i < 32: weights past nsplit are 0)
+            const float w = __shfl_sync(0xffffffffu, wgt, s0 + i);  // (s0 + i < 32: weights past the splits are 0)
             acc.x += v[i].x * w, acc.y += v[i].y * w, acc.z += v[i].z * w, acc.w += v[i].w * w;
         }
     }
@@ -1031,21 +1042,23 @@ int tokens_per_item(int T, int H) {
     return p < 1 ? 1 : (p < T ? p : T);
 }
 
-// Key splits of an item: as many as fill the GPU's CTA pairs, each of at least
-// three tiles, and so many that none is longer than 2^18 keys (as far as 32 splits
-// go): the tensor cores cut off what of a product lies below 2^-25 of the sum it is
-// added to, so the output of n keys of the same sign falls short by n 2^-27
-// (measured, one split: 2e-3 at 2^18, 8e-3 at 2^20, 3.3e-2 at 2^22; 16 splits of
-// the last 2e-3).
-constexpr int kLongTiles = (1 << 18) / kNK;
-int splits(int64_t items, int k) {
+// Key splits of every item: as many as fill the GPU's CTA pairs, each of at least
+// three tiles.
+int base_splits(int64_t items, int k) {
     const int64_t pairs = sm_count() / 2;
     const int tiles = (k + kNK - 1) / kNK;
     int64_t ns = items >= pairs ? 1 : pairs / items;
     if (ns > tiles / 3) ns = tiles / 3;
-    if (ns < (tiles + kLongTiles - 1) / kLongTiles) ns = (tiles + kLongTiles - 1) / kLongTiles;
     if (ns > kMaxSplits) ns = kMaxSplits;
     return ns < 1 ? 1 : static_cast<int>(ns);
+}
+
+// Of the longest item: k may be a bound far above the lengths, so an item takes no
+// more than its own length asks for (64 rows of 4096 positions 115 us; under a bound
+// of 2^20 126, and 171 if they took the bound's splits).
+int most_splits(int64_t items, int k) {
+    const int of_length = static_cast<int>((static_cast<int64_t>(k) + kLongKeys - 1) / kLongKeys);
+    return std::max(base_splits(items, k), std::min(of_length, kMaxSplits));
 }
 
 size_t state_bytes(int64_t items, int ns) { return static_cast<size_t>(items) * ns * 128 * (512 + 2) * 4; }
@@ -1076,7 +1089,7 @@ sa_status launch(const Args& ka, int64_t items, cudaStream_t st) {
 size_t mla_latent_workspace_bytes(int B, int T, int H, int k) {
     const int P = tokens_per_item(T, H);
     const int64_t items = static_cast<int64_t>(B) * ((T + P - 1) / P);
-    const int ns = splits(items, k);
+    const int ns = most_splits(items, k);
     return ns > 1 ? state_bytes(items, ns) : 0;
 }
 
@@ -1086,7 +1099,8 @@ sa_status mla_latent_launch(const LatentArgs& a, void* ws, size_t ws_bytes, cuda
     ka.tokens_per_item = tokens_per_item(a.T, a.H);
     ka.groups = (a.T + ka.tokens_per_item - 1) / ka.tokens_per_item;
     const int64_t items = static_cast<int64_t>(a.B) * ka.groups;
-    ka.nsplit = splits(items, a.k);
+    ka.nsplit = most_splits(items, a.k);
+    ka.base = base_splits(items, a.k);
     ka.items = static_cast<int>(items);
     // Short selections, more of them than pairs, go to the pairs in turn (equal tiles each), so that an item's
     // query and first rows load behind the output before: 500 rows x 128 heads of 64 / 256 / 512 slots take
