@@ -43,7 +43,7 @@
 //    the next item's tiles are under way.
 //
 // Measured (device time, replayed graph): 1024 queries x 2048 selected e4m3 rows x
-// 128 heads in 0.89 ms (656 TFLOP/s), 74 of them (one per pair) in 64 us: 1.56 us
+// 128 heads in 0.90 ms (649 TFLOP/s), 74 of them (one per pair) in 64 us: 1.56 us
 // per tile and 14 us around them.  The tensor cores are at work for 30 percent of
 // that.  What is left is the hand-over from role to role: an earlier version, of
 // 63.6 us, still took 54.4 with conversion, row loads, seven eighths of the products
